@@ -394,7 +394,7 @@ def _own_attn(s):
     if "h" not in s:
         d = bq.attn_desc(_kvdesc(bq, s), c["heads"], c["requests"], s["table"].shape[1], c["max_len"],
                          window=c["window"], q_dtype=_dt(bq, c["q"]), out_dtype=_dt(bq, c["out"]))
-        s["h"] = (d, torch.empty(bq.paged_attn_workspace(d), dtype=torch.uint8, device="cuda"),
+        s["h"] = (d, torch.zeros(bq.paged_attn_workspace(d), dtype=torch.uint8, device="cuda"),
                   torch.empty(s["q"].shape, dtype=TORCH[c["out"]], device="cuda"),
                   torch.empty(s["q"].shape[:2], dtype=torch.float32, device="cuda"))
     d, ws, out, lse = s["h"]
@@ -419,10 +419,11 @@ def _own_w8a8(s):
     import bit_plane_gemv_amd as bq
     c = s["c"]
     if "h" not in s:
-        s["h"] = (bq.w8a8_desc(c["M"], c["N"], c["K"], y_dtype=_dt(bq, c["y"])),
-                  torch.empty((c["M"], c["N"]), dtype=TORCH[c["y"]], device="cuda"))
-    d, y = s["h"]
-    bq.gemm_w8a8(d, s["a"], s["sa"], s["w"], s["sw"], y)
+        d = bq.w8a8_desc(c["M"], c["N"], c["K"], y_dtype=_dt(bq, c["y"]))
+        s["h"] = (d, torch.empty((c["M"], c["N"]), dtype=TORCH[c["y"]], device="cuda"),
+                  torch.zeros(bq.w8a8_workspace(d), dtype=torch.uint8, device="cuda"))
+    d, y, ws = s["h"]
+    bq.gemm_w8a8(d, s["a"], s["sa"], s["w"], s["sw"], y, ws)
     return y
 
 
