@@ -51,6 +51,8 @@ if len(_hip_runtimes()) > 1:
 OK, E_ARG, E_SHAPE, E_ALIGN, E_UNSUPPORTED, E_CAPACITY, E_DEVICE = 0, -1, -2, -3, -4, -5, -6
 SIGN1, RABIT, TERNARY, W2A8, BVSR4, WNAM, HGF = 1, 2, 3, 4, 5, 6, 7
 DT_F32, DT_BF16, DT_ACT, DT_BINARY = 0, 1, 2, 3
+DT_ROW8 = 16       # bitq_block_norm: int8 rows with a scale each
+KV_BF16, KV_INT8 = 0, 1
 F_ACC_INT32 = 1
 F_FUSE_QUANT = 2   # bitq_gemv: raw x, the activation quantizer runs in the GEMV kernel
 
@@ -88,7 +90,37 @@ class Logical(ctypes.Structure):
                 ("lora_b", ctypes.c_void_p), ("lora_alpha", ctypes.c_float)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KvPlanDesc(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int32), ("page", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("ring", ctypes.c_int32), ("tokens", ctypes.c_int32)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("kv", KvDesc), ("heads", ctypes.c_int32), ("requests", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("max_len", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("q_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("u_dtype", ctypes.c_int32),
+                ("r_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("u_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64), ("ro_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("res_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("eps_post", ctypes.c_float), ("eps_pre", ctypes.c_float)]
+
+
+class W8A8Desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("lda", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
 _P = ctypes.c_void_p
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _I32 = ctypes.c_int32
 _U32 = ctypes.c_uint32
@@ -112,6 +144,16 @@ _sigs = {
     "bitq_workspace_size": ([ctypes.POINTER(WDesc), _I32, ctypes.POINTER(_SZ)], _I32),
     "bitq_gemv": ([ctypes.POINTER(WDesc), _P, _P, _I32, _P, _P, _SZ, _U32, _P], _I32),
     "bitq_gemm_smallM": ([ctypes.POINTER(WDesc), _P, _P, _I32, _P, _P, _SZ, _U32, _P], _I32),
+    # operators around the linear layers (include/bitq_lm.h)
+    "bitq_kv_cache_size": ([ctypes.POINTER(KvDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_kv_plan_size": ([ctypes.POINTER(KvPlanDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_kv_plan": ([ctypes.POINTER(KvPlanDesc), _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "bitq_kv_write": ([ctypes.POINTER(KvDesc), _P, _P, _I32, _I64, _I64, _P, _I32, _P, _SZ, _P], _I32),
+    "bitq_paged_attn_workspace": ([ctypes.POINTER(AttnDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_paged_attn": ([ctypes.POINTER(AttnDesc), _P, _I64, _P, _SZ, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "bitq_block_norm": ([ctypes.POINTER(NormDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "bitq_w8a8_workspace": ([ctypes.POINTER(W8A8Desc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_gemm_w8a8": ([ctypes.POINTER(W8A8Desc), _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
     # measurement context kernels (include/bitq_ctx.h)
     "bitq_ctx_empty": ([_I32, _P], _I32),
     "bitq_ctx_stream": ([_P, _SZ, _I32, _P, _I32, _P], _I32),
@@ -351,6 +393,122 @@ def gemm_smallM(desc: WDesc, w, act, M: int, y, ws, ws_bytes: int | None = None,
     nbytes = _nbytes(ws) if ws_bytes is None else ws_bytes
     _check(_lib.bitq_gemm_smallM(ctypes.byref(desc), _ptr(w), _ptr(act), M, _ptr(y), _ptr(ws),
                                  nbytes, flags, _stream(stream)))
+
+
+# ------------------------------------- paged cache, norms, int8 products
+def kvdesc(kv_heads: int, head_dim: int, page: int, pages: int, dtype: int = KV_BF16) -> KvDesc:
+    return KvDesc(kv_heads, head_dim, page, pages, dtype)
+
+
+def _size_of(fn, desc) -> int:
+    n = _SZ(0)
+    _check(fn(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def kv_cache_size(kv: KvDesc) -> int:
+    return _size_of(_lib.bitq_kv_cache_size, kv)
+
+
+def kv_cache_views(kv: KvDesc, cache) -> dict:
+    """Sections of a cache buffer (a uint8 tensor) as tensors: K [pages, heads, page, Dp],
+    V [pages, heads, page / 8, Dp, 8], and for int8 ks, vs [pages, heads, page]."""
+    import torch
+    Dp, P, H, n = (kv.head_dim + 31) // 32 * 32, kv.page, kv.kv_heads, kv.pages
+    t, e = (torch.bfloat16, 2) if kv.dtype == KV_BF16 else (torch.int8, 1)
+    size = n * H * P * Dp * e
+    sec = (size + 255) // 256 * 256
+    out = dict(K=cache[:size].view(t).view(n, H, P, Dp), V=cache[sec:sec + size].view(t).view(n, H, P // 8, Dp, 8))
+    if kv.dtype == KV_INT8:
+        sc = 4 * n * H * P
+        at = 2 * sec
+        out["ks"] = cache[at:at + sc].view(torch.float32).view(n, H, P)
+        at += (sc + 255) // 256 * 256
+        out["vs"] = cache[at:at + sc].view(torch.float32).view(n, H, P)
+    return out
+
+
+def kv_plan_desc(requests: int, page: int, table_stride: int, ring: int, tokens: int) -> KvPlanDesc:
+    return KvPlanDesc(requests, page, table_stride, ring, tokens)
+
+
+def kv_plan_size(desc: KvPlanDesc) -> int:
+    return _size_of(_lib.bitq_kv_plan_size, desc)
+
+
+def kv_plan_views(desc: KvPlanDesc, plan) -> dict:
+    """Sections of a plan buffer (a uint8 tensor) as int32 tensors: state, len, start, slot, req, pos."""
+    import torch
+    out, at = {}, 0
+    for name, n in (("state", 4), ("len", desc.requests), ("start", desc.requests + 1), ("slot", desc.tokens),
+                    ("req", desc.tokens), ("pos", desc.tokens)):
+        out[name] = plan[at:at + 4 * n].view(torch.int32)
+        at += (4 * n + 255) // 256 * 256
+    return out
+
+
+def kv_plan(desc: KvPlanDesc, old_len, new_len, ring, state, table, plan, stream=None):
+    """One scheduling step: pages from and to the ring, tables, slots (bitq_kv_plan)."""
+    _check(_lib.bitq_kv_plan(desc, _ptr(old_len), _ptr(new_len), _ptr(ring), _ptr(state), _ptr(table), _ptr(plan),
+                             _nbytes(plan), _stream(stream)))
+
+
+def kv_write(kv: KvDesc, k, v, x_dtype: int, slots, cache, tokens: int | None = None, k_stride: int | None = None,
+             v_stride: int | None = None, stream=None):
+    """Keys and values of new tokens into their slots (bitq_kv_write).  k, v: tensors [tokens, kv_heads,
+    head_dim] whose last two dimensions are contiguous (or addresses, with the strides given)."""
+    _check(_lib.bitq_kv_write(kv, _ptr(k), _ptr(v), x_dtype, k.stride(0) if k_stride is None else k_stride,
+                              v.stride(0) if v_stride is None else v_stride, _ptr(slots),
+                              slots.numel() if tokens is None else tokens, _ptr(cache), _nbytes(cache), _stream(stream)))
+
+
+def attn_desc(kv: KvDesc, heads: int, requests: int, table_stride: int, max_len: int, window: int = 0,
+              q_dtype: int = DT_BF16, out_dtype: int = DT_BF16, scale: float | None = None) -> AttnDesc:
+    return AttnDesc(kv, heads, requests, table_stride, max_len, window, q_dtype, out_dtype,
+                    kv.head_dim ** -0.5 if scale is None else scale)
+
+
+def paged_attn_workspace(desc: AttnDesc) -> int:
+    return _size_of(_lib.bitq_paged_attn_workspace, desc)
+
+
+def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_stride: int | None = None,
+               ws_bytes: int | None = None, stream=None):
+    """Attention of one new token per request over the paged cache (bitq_paged_attn)."""
+    _check(_lib.bitq_paged_attn(desc, _ptr(q), q.stride(0) if q_stride is None else q_stride, _ptr(cache),
+                                _nbytes(cache), _ptr(table), _ptr(lens), _ptr(out), _ptr(lse), _ptr(ws),
+                                _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def norm_desc(rows: int, width: int, u_dtype: int = DT_F32, r_dtype: int = DT_F32, w_dtype: int = DT_F32,
+              out_dtype: int = DT_F32, res_scale: float = 1.0, branch_scale: float = 1.0, eps_post: float = 1e-5,
+              eps_pre: float = 1e-5, gate_stride: int = 0, u_stride: int | None = None, r_stride: int | None = None,
+              ro_stride: int | None = None, h_stride: int | None = None) -> NormDesc:
+    st = [width if s is None else s for s in (u_stride, r_stride, ro_stride, h_stride)]
+    return NormDesc(rows, width, u_dtype, r_dtype, w_dtype, out_dtype, *st, gate_stride, res_scale, branch_scale,
+                    eps_post, eps_pre)
+
+
+def block_norm(desc: NormDesc, u, r, post, gate, pre, r_out, h, d=None, stream=None):
+    """Residual update with the norms before and after it (bitq_block_norm); d: the rows' scales (DT_ROW8)."""
+    _check(_lib.bitq_block_norm(desc, _ptr(u), _ptr(r), _ptr(post), _ptr(gate), _ptr(pre), _ptr(r_out), _ptr(h),
+                                _ptr(d), _stream(stream)))
+
+
+def w8a8_desc(M: int, N: int, K: int, y_dtype: int = DT_F32, lda: int | None = None, ldw: int | None = None,
+              ldy: int | None = None, flags: int = 0) -> W8A8Desc:
+    return W8A8Desc(M, N, K, y_dtype, K if lda is None else lda, K if ldw is None else ldw,
+                    N if ldy is None else ldy, flags)
+
+
+def w8a8_workspace(desc: W8A8Desc) -> int:
+    return _size_of(_lib.bitq_w8a8_workspace, desc)
+
+
+def gemm_w8a8(desc: W8A8Desc, a, a_scale, w, w_scale, y, ws=None, ws_bytes: int | None = None, stream=None):
+    """y = diag(a_scale) a w^T diag(w_scale) on int8 rows (bitq_gemm_w8a8)."""
+    _check(_lib.bitq_gemm_w8a8(desc, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(y), _ptr(ws),
+                               _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------- measurement context kernels

@@ -66,6 +66,11 @@ def _run_all(cmds, jobs: int):
         raise RuntimeError("command failed: " + " ".join(failed))
 
 
+def host_sources() -> list:
+    """The host-only C++ sources of the library."""
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cpp"))
+
+
 def kernel_sources() -> list:
     """The HIP sources of the library (one per kernel family)."""
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
@@ -73,11 +78,11 @@ def kernel_sources() -> list:
 
 def build(asm: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     jobs = jobs or max(1, min(8, os.cpu_count() or 1))
-    host_src = os.path.join(CSRC, "bitq_host.cpp")
     cmds, objs = [], []
-    host_obj = os.path.join(CSRC, "bitq_host.o")
-    cmds.append([HIPCC, *COMMON, "-c", host_src, "-o", host_obj])
-    objs.append(host_obj)
+    for src in host_sources():
+        obj = src[:-4] + ".o"
+        cmds.append([HIPCC, *COMMON, "-c", src, "-o", obj])
+        objs.append(obj)
     for src in kernel_sources():
         obj = src[:-4] + ".o"
         cmds.append([HIPCC, *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c", src, "-o", obj])
@@ -116,12 +121,13 @@ def build_sanitized(verbose: bool = False, jobs: int | None = None) -> str:
 
     The kernels themselves are not instrumented (device code); only host code is."""
     jobs = jobs or max(1, min(8, os.cpu_count() or 1))
-    host_src = os.path.join(CSRC, "bitq_host.cpp")
-    host_obj = os.path.join(CSRC, "bitq_host_san.o")
     inc = f"-I{os.path.join(HERE, '..', 'include')}"
-    cmds = [["g++", "-O1", "-g", "-std=c++17", "-fPIC", "-ffp-contract=off", "-D__HIP_PLATFORM_AMD__", inc,
-             "-I/opt/rocm/include", *SAN_FLAGS, "-c", host_src, "-o", host_obj]]
-    objs = [host_obj]
+    cmds, objs = [], []
+    for src in host_sources():
+        obj = src[:-4] + "_san.o"
+        cmds.append(["g++", "-O1", "-g", "-std=c++17", "-fPIC", "-ffp-contract=off", "-D__HIP_PLATFORM_AMD__", inc,
+                     "-I/opt/rocm/include", *SAN_FLAGS, "-c", src, "-o", obj])
+        objs.append(obj)
     for src in kernel_sources():
         obj = src[:-4] + "_san.o"
         cmds.append([HIPCC, *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c", src, "-o", obj])

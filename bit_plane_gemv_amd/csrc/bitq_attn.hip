@@ -1,0 +1,646 @@
+// Attention of one new token per request over the paged cache of libbitq.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+
+#include "bitq_device.h"
+
+namespace bitq {
+
+// out = sum_t p_t V_t / sum_t p_t, p_t = exp(scale q . K_t): every key and
+// value is read once and used for the `group` query heads that share it, so
+// the kernel is bound by the memory stream.  One pass: each wave keeps a
+// running maximum m, sum l and accumulator O per query head, in fp32, and
+// rescales O and l when m grows.
+//
+// Matrix cores.  A wave takes steps of 32 tokens of one key-value head and a
+// tile of 16 query heads:
+//   S[32 tokens][16 heads] = K q^T   (two 16-token tiles, A = K rows)
+//   O^T[Dp][16 heads] += V^T P       (A = V^T, B = P)
+// with v_mfma_f32_16x16x32_bf16: lane l = 16 g + j holds 8 consecutive k of
+// row (column) j of A (B), and rows 4 g + i, i < 4, of column j of D.  Row
+// 4 g + i of score tile t is given token 8 g + 4 t + i, so that a lane's 8
+// scores are those of 8 consecutive tokens 8 g .. 8 g + 7 of head j: exactly
+// the B operand that the second product needs from that lane, with no
+// movement between lanes.  V's layout (8 tokens of an element together) makes
+// its A operand one 16-byte load.  All operands go from memory to registers;
+// LDS is used only to join the waves at the end.  With fewer than 16 query
+// heads per key-value head columns idle: the matrix cores need a tenth of the
+// memory's time even so.
+//
+// Precision.  bf16 and int8 cache rows are exact in bf16; int8 scales are
+// applied in fp32, to the scores and to p.  fp32 q is split into 3 bf16
+// terms (exact), bf16 q needs one.  p is split into 2 terms (relative
+// rounding 2^-17, below half an ulp of a bf16 output) or, when q or the output is
+// fp32, into 3 (2^-25).  Everything else is fp32.
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+    const void* q;
+    const uint8_t* cache;
+    const int32_t* table;
+    const int32_t* lens;
+    void* out;
+    float* lse;
+    float* part;       // split: partial results, two per workgroup
+    int32_t* prefix;   // split: [R + 1] prefix sums of the requests' units
+    int64_t q_stride;
+    size_t off_v, off_ks, off_vs;
+    int R, H, A, group, tiles, D, page_shift, pages, table_stride, max_len, window;
+    float c;           // scale log2(e): p = 2^(c s - m)
+    int qdt, odt;
+    bool qvec;         // 8-element chunks of q are 16-byte aligned
+};
+
+// Tokens [lo, hi) of request r.
+__device__ __forceinline__ void token_range(const AttnArgs& a, int r, int& lo, int& hi) {
+    hi = min(max(a.lens[r], 0), a.max_len);
+    lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+}
+// Passes of a workgroup over [lo, hi): steps are aligned to 32 tokens.
+__device__ __forceinline__ int token_units(int lo, int hi) {
+    return hi > lo ? (hi - (lo & ~31) + kAttnUnit - 1) / kAttnUnit : 0;
+}
+
+// Maximum / sum over the four lanes 16 g + j of a column.
+__device__ __forceinline__ float col_max(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float col_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// x = sum of the N bf16 terms, each the rounding of what the ones before leave
+template <int N>
+__device__ __forceinline__ void split_terms(const float (&x)[8], bf16x8_t (&t)[N]) {
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            t[n][e] = static_cast<__bf16>(r[e]);
+            r[e] -= static_cast<float>(t[n][e]);
+        }
+}
+
+// 8 int8 codes as bf16 (exact)
+__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t lo, uint32_t hi) {
+    bf16x8_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(lo >> (8 * e))));
+        v[4 + e] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(hi >> (8 * e))));
+    }
+    return v;
+}
+
+// What a wave reads for one step of 32 tokens, as loaded.
+template <int KVT, int NC>
+struct AttnStep {
+    uint4 k[2][KVT == BITQ_KV_BF16 ? NC : (NC + 1) / 2];
+    uint4 v[KVT == BITQ_KV_BF16 ? 2 * NC : NC];
+    float4 ks[KVT == BITQ_KV_INT8 ? 2 : 1], vs[KVT == BITQ_KV_INT8 ? 2 : 1];
+};
+
+template <int KVT, int NC, bool HI>
+struct AttnWave {
+    static constexpr int NQ = HI ? 3 : 1, NP = HI ? 3 : 2, Dp = 32 * NC;
+    static constexpr bool I8 = KVT == BITQ_KV_INT8;
+    bf16x8_t q[NQ][NC];
+    f32x4_t o[2 * NC];
+    float m, l;
+    const AttnArgs& a;
+    const int lane, g, j;
+    const int32_t* row;  // the request's row of the table
+    int h, lo, hi;
+
+    __device__ __forceinline__ AttnWave(const AttnArgs& args, int ln)
+        : a(args), lane(ln), g(ln >> 4), j(ln & 15) {}
+
+    // Element of the row at which lane group g's k positions of chunk c begin.
+    // bf16: 32 c + 8 g.  int8: a lane's 16-byte load covers two chunks.
+    static __device__ __forceinline__ int chunk_elem(int c, int g) {
+        if (I8 && (c | 1) < NC) return 64 * (c >> 1) + 16 * g + 8 * (c & 1);
+        return 32 * c + 8 * g;
+    }
+
+    __device__ __forceinline__ void begin(int r, int hk, int tile, int lo_, int hi_) {
+        h = hk;
+        lo = lo_;
+        hi = hi_;
+        row = a.table + static_cast<size_t>(r) * a.table_stride;
+        const int head = 16 * tile + j;
+        const bool live = head < a.group;
+        const int64_t at = static_cast<int64_t>(r) * a.q_stride + (static_cast<int64_t>(hk) * a.group + (live ? head : 0)) * a.D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int d = chunk_elem(c, g);
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (live && d < a.D) {
+                if (a.qvec) {  // (D is a multiple of 8 then)
+                    if (a.qdt == BITQ_DT_F32) {
+                        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + d);
+                        const float4 u = p[0], w = p[1];
+                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                        x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+                    } else {
+                        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[2 * e] = __uint_as_float(w[e] << 16);
+                            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (d + e < a.D) x[e] = load_act(a.q, a.qdt, static_cast<size_t>(at + d + e));
+                }
+            }
+            bf16x8_t t[NQ];
+            split_terms<NQ>(x, t);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) q[n][c] = t[n];
+        }
+#pragma unroll
+        for (int c = 0; c < 2 * NC; ++c) o[c] = f32x4_t{0, 0, 0, 0};
+        m = -FLT_MAX;
+        l = 0.0f;
+    }
+
+    // Tokens whose data this lane loads for the step at token s, kept inside
+    // [lo, hi) (what lies outside is masked in compute): K rows of the two
+    // tiles, V group (and scales).
+    __device__ __forceinline__ void tokens(int s, int (&tok)[3]) const {
+        const int k = s + 8 * (j >> 2) + (j & 3);
+        tok[0] = min(max(k, lo), hi - 1);
+        tok[1] = min(max(k + 4, lo), hi - 1);
+        tok[2] = min(max(s + 8 * g, lo & ~7), (hi - 1) & ~7);
+    }
+    __device__ __forceinline__ void lookup(int s, int (&pg)[3]) const {
+        int tok[3];
+        tokens(s, tok);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) pg[i] = row[tok[i] >> a.page_shift];
+    }
+
+    __device__ __forceinline__ void load(int s, const int (&pg)[3], AttnStep<KVT, NC>& L) const {
+        constexpr int es = I8 ? 1 : 2;
+        int tok[3];
+        tokens(s, tok);
+        const int P = 1 << a.page_shift;
+        size_t at[3];  // row of the pool
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int p = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.pages) ? pg[i] : 0;
+            at[i] = ((static_cast<size_t>(p) * a.H + h) << a.page_shift) + (tok[i] & (P - 1));
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* kp = a.cache + at[t] * (Dp * es);
+            if constexpr (!I8) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) L.k[t][c] = *reinterpret_cast<const uint4*>(kp + 64 * c + 16 * g);
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC / 2; ++c) L.k[t][c] = *reinterpret_cast<const uint4*>(kp + 64 * c + 16 * g);
+                if constexpr (NC % 2) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(kp + 32 * (NC - 1) + 8 * g);
+                    L.k[t][NC / 2] = make_uint4(u.x, u.y, 0, 0);
+                }
+            }
+        }
+        const uint8_t* vp = a.cache + a.off_v + at[2] * (Dp * es);  // (groups of 8 rows: at[2] is a multiple of 8)
+        if constexpr (!I8) {
+#pragma unroll
+            for (int c = 0; c < 2 * NC; ++c) L.v[c] = *reinterpret_cast<const uint4*>(vp + 256 * c + 16 * j);
+        } else {
+            // 16 bytes: elements 32 c + 2 j and 32 c + 2 j + 1 of 8 tokens
+#pragma unroll
+            for (int c = 0; c < NC; ++c) L.v[c] = *reinterpret_cast<const uint4*>(vp + 256 * c + 16 * j);
+            const float4* ksp = reinterpret_cast<const float4*>(a.cache + a.off_ks) + at[2] / 4;
+            const float4* vsp = reinterpret_cast<const float4*>(a.cache + a.off_vs) + at[2] / 4;
+            L.ks[0] = ksp[0];
+            L.ks[1] = ksp[1];
+            L.vs[0] = vsp[0];
+            L.vs[1] = vsp[1];
+        }
+    }
+
+    __device__ __forceinline__ void compute(int s, const AttnStep<KVT, NC>& L) {
+        float x[8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                bf16x8_t kf;
+                if constexpr (!I8) {
+                    kf = __builtin_bit_cast(bf16x8_t, L.k[t][c]);
+                } else {
+                    const uint4 u = L.k[t][c >> 1];
+                    kf = (c & 1) ? codes_bf16(u.z, u.w) : codes_bf16(u.x, u.y);
+                }
+#pragma unroll
+                for (int n = NQ - 1; n >= 0; --n)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][c], acc, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * t + i] = acc[i];
+        }
+        // scores of tokens s + 8 g + e; masked ones become -inf
+        const bool edge = s < lo || s + 32 > hi;  // (the same for the whole wave)
+        if constexpr (I8) {
+            const float ks[8] = {L.ks[0].x, L.ks[0].y, L.ks[0].z, L.ks[0].w, L.ks[1].x, L.ks[1].y, L.ks[1].z, L.ks[1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= ks[e];
+        }
+        uint32_t keep = 0xFFu;  // bit e: token s + 8 g + e is in [lo, hi)
+        if (edge) {
+            keep = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int tk = s + 8 * g + e;
+                if (tk >= lo && tk < hi) keep |= 1u << e;
+            }
+        }
+        float mx = -FLT_MAX;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] *= a.c;
+            if (edge && !(keep & (1u << e))) x[e] = -INFINITY;
+            mx = fmaxf(mx, x[e]);
+        }
+        mx = col_max(mx);
+        if (__any(mx > m)) {
+            const float mn = fmaxf(m, mx);
+            const float f = exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < 2 * NC; ++c) o[c] *= f;
+        }
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = exp2f(x[e] - m);
+            l += p[e];
+        }
+        if constexpr (I8) {
+            const float vs[8] = {L.vs[0].x, L.vs[0].y, L.vs[0].z, L.vs[0].w, L.vs[1].x, L.vs[1].y, L.vs[1].z, L.vs[1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = (edge && !(keep & (1u << e))) ? 0.0f : p[e] * vs[e];
+        }
+        bf16x8_t pf[NP];
+        split_terms<NP>(p, pf);
+#pragma unroll
+        for (int c = 0; c < 2 * NC; ++c) {
+            bf16x8_t vf;
+            if constexpr (!I8) {
+                uint4 u = L.v[c];
+                if (edge) {  // what lies in masked places may be infinite or NaN: 0 p must stay 0
+                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!(keep & (1u << e))) w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                    u = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                vf = __builtin_bit_cast(bf16x8_t, u);
+            } else {
+                const uint4 u = L.v[c >> 1];  // (int8 codes are finite whatever the bytes)
+                vf = (c & 1) ? codes_bf16(u.z, u.w) : codes_bf16(u.x, u.y);
+            }
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n)
+                o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[c], 0, 0, 0);
+        }
+    }
+
+    // The wave's steps s0, s0 + stride, ... below s1, loads one step ahead.
+    __device__ __forceinline__ void run(int s0, int s1, int stride) {
+        if (s0 >= s1) return;
+        AttnStep<KVT, NC> A;
+        int pg[3];
+        lookup(s0, pg);
+        for (int s = s0; s < s1; s += stride) {
+            load(s, pg, A);
+            if (s + stride < s1) lookup(s + stride, pg);
+            compute(s, A);
+        }
+    }
+
+    // O, m, l to the wave's part of LDS: so [16][Dp + 4], sm and sl [16].
+    __device__ __forceinline__ void park(float* so, float* sm, float* sl) {
+        l = col_sum(l);
+        if (g == 0) {
+            sm[j] = m;
+            sl[j] = l;
+        }
+        float* r = so + j * (Dp + 4);
+        if constexpr (!I8) {
+#pragma unroll
+            for (int c = 0; c < 2 * NC; ++c) *reinterpret_cast<f32x4_t*>(r + 16 * c + 4 * g) = o[c];
+        } else {
+            // tile 2c + b, row 4 g + i is element 32 c + 2 (4 g + i) + b
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const f32x4_t u = o[2 * c], w = o[2 * c + 1];
+                *reinterpret_cast<f32x4_t*>(r + 32 * c + 8 * g) = f32x4_t{u[0], w[0], u[1], w[1]};
+                *reinterpret_cast<f32x4_t*>(r + 32 * c + 8 * g + 4) = f32x4_t{u[2], w[2], u[3], w[3]};
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void store_out(const AttnArgs& a, size_t i, float v) {
+    if (a.odt == BITQ_DT_F32) static_cast<float*>(a.out)[i] = v;
+    else static_cast<uint16_t*>(a.out)[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// First index i in [0, n) with a[i] > x (n if none); a ascending.
+__device__ __forceinline__ int first_above64(const int32_t* a, int n, int64_t x) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// SPLIT = false: workgroup = one item (request, key-value head, tile of 16 of
+// its query heads), its tokens dealt to the waves in steps of 32.
+// SPLIT = true: the items' tokens, in units of 128, are laid end to end (head
+// tiles outermost, then requests) and dealt to the gridDim.x workgroups in
+// equal contiguous ranges, so ragged lengths load every workgroup alike.
+// A range that covers an item whole writes its output; the ends of an item
+// that lies in several ranges go to the workgroup's two partial results (slot
+// 0: an item begun elsewhere, slot 1: one begun here) for the join kernel.
+template <int KVT, int NC, bool HI, bool SPLIT>
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void paged_attn_kernel(AttnArgs a) {
+    constexpr int Dp = 32 * NC, W = kAttnWaves, ROW = Dp + 4;
+    __shared__ __align__(16) float s_o[W][16 * ROW];
+    __shared__ float s_m[W][16], s_l[W][16];
+    extern __shared__ int32_t s_pre[];  // SPLIT: [R + 1]
+    __shared__ int32_t s_scan[W];
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
+    const int HT = a.H * a.tiles;
+    AttnWave<KVT, NC, HI> w(a, lane);
+
+    int64_t x = blockIdx.x, x1 = static_cast<int64_t>(blockIdx.x) + 1;  // units (SPLIT) or the item
+    int64_t U = 1;
+    if constexpr (SPLIT) {
+        int carry = 0;
+        for (int r0 = 0; r0 < a.R; r0 += 64 * W) {
+            const int r = r0 + tid;
+            int u = 0;
+            if (r < a.R) {
+                int lo, hi;
+                token_range(a, r, lo, hi);
+                u = token_units(lo, hi);
+            }
+            int inc = u;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int t = __shfl_up(inc, o, 64);
+                if (lane >= o) inc += t;
+            }
+            __syncthreads();
+            if (lane == 63) s_scan[wave] = inc;
+            __syncthreads();
+            int all = 0;
+            for (int i = 0; i < W; ++i) {
+                if (i < wave) inc += s_scan[i];
+                all += s_scan[i];
+            }
+            if (r < a.R) s_pre[r + 1] = carry + inc;
+            carry += all;
+        }
+        if (tid == 0) s_pre[0] = 0;
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int r = tid; r <= a.R; r += 64 * W) a.prefix[r] = s_pre[r];
+        U = s_pre[a.R];
+        const int64_t T = U * HT;
+        // (with fewer units than workgroups the surplus workgroups have none:
+        // every range below G is non-empty, which the join relies on)
+        const int64_t G = min(T, static_cast<int64_t>(gridDim.x));
+        if (blockIdx.x >= G) return;
+        x = T * blockIdx.x / G;
+        x1 = T * (static_cast<int64_t>(blockIdx.x) + 1) / G;
+    }
+    while (x < x1) {
+        int ht, r, lo, hi, s0, s1;
+        bool whole = true;
+        int slot = 0;
+        int64_t next = x + 1;
+        if constexpr (SPLIT) {
+            ht = static_cast<int>(x / U);
+            const int64_t rem = x - ht * U;
+            r = first_above64(s_pre + 1, a.R, rem);
+            token_range(a, r, lo, hi);
+            const int64_t end = ht * U + s_pre[r + 1];
+            next = min(x1, end);
+            const int64_t k0 = rem - s_pre[r];
+            whole = k0 == 0 && next == end;
+            slot = k0 == 0 ? 1 : 0;
+            s0 = (lo & ~31) + static_cast<int>(k0) * kAttnUnit;
+            s1 = static_cast<int>(min(static_cast<int64_t>(hi), s0 + (next - x) * kAttnUnit));
+        } else {
+            ht = static_cast<int>(x % HT);
+            r = static_cast<int>(x / HT);
+            token_range(a, r, lo, hi);
+            s0 = lo & ~31;
+            s1 = hi;
+        }
+        // (values that are the same for the whole wave, kept in scalar registers)
+        ht = wave_uniform(ht);
+        r = wave_uniform(r);
+        const int hk = ht / a.tiles, tile = ht - hk * a.tiles;
+        w.begin(r, hk, tile, wave_uniform(lo), wave_uniform(hi));
+        w.run(wave_uniform(s0) + 32 * wave, wave_uniform(s1), kAttnUnit);
+        w.park(s_o[wave], s_m[wave], s_l[wave]);
+        __syncthreads();
+        const int heads = min(16, a.group - 16 * tile);
+        float* part = SPLIT ? a.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (16 * (Dp + 2)) : nullptr;
+        for (int i = tid; i < heads * Dp; i += 64 * W) {
+            const int head = i / Dp, d = i - head * Dp;
+            float M = s_m[0][head];
+#pragma unroll
+            for (int v = 1; v < W; ++v) M = fmaxf(M, s_m[v][head]);
+            float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+            for (int v = 0; v < W; ++v) {
+                const float f = exp2f(s_m[v][head] - M);
+                sum += f * s_l[v][head];
+                acc += f * s_o[v][head * ROW + d];
+            }
+            if (whole) {
+                const size_t qa = static_cast<size_t>(r) * a.A + static_cast<size_t>(hk) * a.group + 16 * tile + head;
+                if (d < a.D) store_out(a, qa * a.D + d, sum == 0.0f ? 0.0f : acc / sum);
+                if (d == 0 && a.lse) a.lse[qa] = lse_of(M, sum);
+            } else {
+                part[head * Dp + d] = acc;
+                if (d == 0) {
+                    part[16 * Dp + head] = M;
+                    part[16 * Dp + 16 + head] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        x = next;
+    }
+}
+
+// Joins the partial results of the items that lie in several workgroups'
+// ranges, and writes the outputs of requests without tokens.  NW waves per
+// query head: one when there are many heads (4 heads a workgroup), 16 when
+// there are few and an item may lie in hundreds of ranges.
+template <int NW>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void attn_join_kernel(AttnArgs a, int Dp, int main_grid) {
+    constexpr int HPB = NW == 1 ? 4 : 1;
+    __shared__ float s_acc[NW][256], s_m[NW], s_l[NW];
+    const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
+    const int64_t qa = static_cast<int64_t>(blockIdx.x) * HPB + (NW == 1 ? wave : 0);
+    if (qa >= static_cast<int64_t>(a.R) * a.A) return;
+    const int r = static_cast<int>(qa / a.A), qh = static_cast<int>(qa - static_cast<int64_t>(r) * a.A);
+    const int hk = qh / a.group, in = qh - hk * a.group, ht = hk * a.tiles + (in >> 4), head = in & 15;
+    const int64_t U = a.prefix[a.R], u0 = a.prefix[r], u1 = a.prefix[r + 1];
+    float acc[4] = {0, 0, 0, 0}, M = -FLT_MAX, L = 0.0f;
+    if (u1 > u0) {
+        const int64_t T = U * a.H * a.tiles, b = ht * U, G = min(T, static_cast<int64_t>(main_grid));
+        // the workgroup whose range [T i / G, T (i + 1) / G) holds unit x is
+        // the largest i with T i / G < x + 1
+        const int64_t i0 = ((b + u0 + 1) * G - 1) / T, i1 = ((b + u1) * G - 1) / T;
+        if (i0 == i1) return;  // whole in one range: written there
+        for (int64_t i = i0 + (NW == 1 ? 0 : wave); i <= i1; i += NW) {
+            const float* p = a.part + (static_cast<size_t>(i) * 2 + (i == i0 ? 1 : 0)) * (16 * (Dp + 2));
+            const float pm = p[16 * Dp + head], pl = p[16 * Dp + 16 + head];
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = lane + 64 * e < Dp ? p[head * Dp + lane + 64 * e] : 0.0f;
+            const float mn = fmaxf(M, pm), f = exp2f(M - mn), fp = exp2f(pm - mn);
+            M = mn;
+            L = L * f + pl * fp;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f + v[e] * fp;
+        }
+    }
+    if constexpr (NW > 1) {
+        if (lane == 0) {
+            s_m[wave] = M;
+            s_l[wave] = L;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_acc[wave][lane + 64 * e] = acc[e];
+        __syncthreads();
+        if (wave != 0) return;
+        M = s_m[0];
+        for (int v = 1; v < NW; ++v) M = fmaxf(M, s_m[v]);
+        L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
+        for (int v = 0; v < NW; ++v) {
+            const float f = exp2f(s_m[v] - M);
+            L += f * s_l[v];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += f * s_acc[v][lane + 64 * e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int d = lane + 64 * e;
+        if (d < a.D) store_out(a, static_cast<size_t>(qa) * a.D + d, L == 0.0f ? 0.0f : acc[e] / L);
+    }
+    if (lane == 0 && a.lse) a.lse[qa] = lse_of(M, L);
+}
+
+template <int KVT, int NC, bool HI>
+static void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * kAttnWaves);
+    if (!p.split) {
+        hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false>), grid, block, 0, st, a);
+        return;
+    }
+    hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, true>), grid, block, 4 * (static_cast<size_t>(a.R) + 1), st, a);
+    const int64_t heads = static_cast<int64_t>(a.R) * a.A;
+    if (heads <= 512)
+        hipLaunchKernelGGL(attn_join_kernel<16>, dim3(static_cast<unsigned>(heads)), dim3(1024), 0, st, a, p.Dp, p.grid);
+    else
+        hipLaunchKernelGGL(attn_join_kernel<1>, dim3(static_cast<unsigned>((heads + 3) / 4)), dim3(256), 0, st, a, p.Dp, p.grid);
+}
+
+template <int KVT, bool HI>
+static void launch_attn_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+    switch (p.Dp / 32) {
+        case 1: launch_attn<KVT, 1, HI>(a, p, st); break;
+        case 2: launch_attn<KVT, 2, HI>(a, p, st); break;
+        case 3: launch_attn<KVT, 3, HI>(a, p, st); break;
+        case 4: launch_attn<KVT, 4, HI>(a, p, st); break;
+        case 5: launch_attn<KVT, 5, HI>(a, p, st); break;
+        case 6: launch_attn<KVT, 6, HI>(a, p, st); break;
+        case 7: launch_attn<KVT, 7, HI>(a, p, st); break;
+        default: launch_attn<KVT, 8, HI>(a, p, st); break;
+    }
+}
+
+int launch_paged_attn(const bitq_attn_desc& d, const AttnPlan& plan, const void* q, int64_t q_stride,
+                      const void* cache, const int32_t* table, const int32_t* lens, void* out, float* lse, void* ws,
+                      void* stream) {
+    const KvLayout L = kv_layout(d.kv);
+    AttnArgs a{};
+    a.q = q;
+    a.cache = static_cast<const uint8_t*>(cache);
+    a.table = table;
+    a.lens = lens;
+    a.out = out;
+    a.lse = lse;
+    a.prefix = static_cast<int32_t*>(ws);
+    a.part = plan.split ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.off_part) : nullptr;
+    a.q_stride = q_stride;
+    a.off_v = L.off_v;
+    a.off_ks = L.off_ks;
+    a.off_vs = L.off_vs;
+    a.R = d.requests;
+    a.H = d.kv.kv_heads;
+    a.A = d.heads;
+    a.group = plan.group;
+    a.tiles = plan.tiles;
+    a.D = d.kv.head_dim;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(d.kv.page));
+    a.pages = d.kv.pages;
+    a.table_stride = d.table_stride;
+    a.max_len = d.max_len;
+    a.window = d.window;
+    a.c = d.scale * 1.44269504088896340736f;
+    a.qdt = d.q_dtype;
+    a.odt = d.out_dtype;
+    const int per = d.q_dtype == BITQ_DT_F32 ? 4 : 8;
+    a.qvec = aligned(q, 16) && q_stride % per == 0 && d.kv.head_dim % 8 == 0;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    if (d.kv.dtype == BITQ_KV_BF16) {
+        if (hi) launch_attn_dim<BITQ_KV_BF16, true>(a, plan, st);
+        else launch_attn_dim<BITQ_KV_BF16, false>(a, plan, st);
+    } else {
+        if (hi) launch_attn_dim<BITQ_KV_INT8, true>(a, plan, st);
+        else launch_attn_dim<BITQ_KV_INT8, false>(a, plan, st);
+    }
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace bitq

@@ -122,5 +122,13 @@ __device__ __forceinline__ uint4 buffer_load_u128(__amdgpu_buffer_rsrc_t r, uint
     const v4u v = __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(voff), static_cast<int>(soff), 0);
     return make_uint4(v.x, v.y, v.z, v.w);
 }
+// 16 bytes per lane from memory straight into LDS: lane l's bytes land at
+// dst + 16 l (dst is wave-uniform).  Out-of-range offsets store zeros.
+__device__ __forceinline__ void buffer_copy_lds16(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff) {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass does not know the builtin)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
+                                             static_cast<int>(voff), 0, 0, 0);
+#endif
+}
 
 }  // namespace bitq

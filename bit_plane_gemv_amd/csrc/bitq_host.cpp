@@ -10,7 +10,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
 #include <thread>
 #include <vector>
 
@@ -18,25 +17,23 @@
 
 namespace bitq {
 namespace {
-
-thread_local std::string g_error;
+thread_local char g_error[512];  // (a fixed buffer: setting it cannot throw)
+}  // namespace
 
 bitq_status fail(bitq_status s, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    vsnprintf(g_error, sizeof(g_error), fmt, ap);
     va_end(ap);
-    g_error = buf;
     return s;
 }
 
 bitq_status ok() {
-    g_error.clear();
+    g_error[0] = 0;
     return BITQ_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 // ------------------------------------------------------------- fp16 helpers
 // IEEE binary16 from a double, round-half-to-even, with subnormals and
@@ -895,7 +892,7 @@ extern "C" {
 
 int32_t bitq_version(void) { return BITQ_VERSION; }
 
-const char* bitq_last_error(void) { return g_error.c_str(); }
+const char* bitq_last_error(void) { return g_error; }
 
 bitq_status bitq_packed_size(const bitq_wdesc* desc, size_t* bytes) {
     bitq_status s = check_desc(desc);

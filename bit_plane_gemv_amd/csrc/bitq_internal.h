@@ -7,6 +7,7 @@
 
 #include "../../include/bitq.h"
 #include "../../include/bitq_ctx.h"
+#include "../../include/bitq_lm.h"
 
 namespace bitq {
 
@@ -28,6 +29,11 @@ constexpr int kMaxHgfK = 63 * 256;  // HGF: <= 63 runs of 256 inputs meet in one
 // input (e >> 1) + 4 (e & 1) of the word's 8 inputs (the order in which two
 // words of 4 activation bytes split into nibble words most cheaply)
 constexpr int bvsr_nibble_input(int e) { return (e >> 1) + 4 * (e & 1); }
+
+// The calling thread's error text (bitq_last_error): set and return s; clear.
+bitq_status fail(bitq_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+bitq_status ok();
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -148,6 +154,72 @@ int launch_gemv_xnor(const bitq_wdesc& d, const void* w, const void* act, int M,
 int launch_ctx_empty(int grid, void* stream);
 int launch_ctx_stream(const void* src, size_t bytes, int grid, float* out, int nout, void* stream);
 int launch_ctx_spin(int microseconds, void* stream);
+
+// ------------------------------------------------- operators of bitq_lm.h
+// Byte layout of a cache buffer; strides in elements of the rows.
+struct KvLayout {
+    int Dp;
+    size_t off_v, off_ks, off_vs, total;
+};
+inline KvLayout kv_layout(const bitq_kvdesc& kv) {
+    KvLayout L{};
+    L.Dp = static_cast<int>(round_up(kv.head_dim, 32));
+    const size_t rows = static_cast<size_t>(kv.pages) * kv.page * kv.kv_heads;
+    const size_t sec = align256(rows * L.Dp * (kv.dtype == BITQ_KV_BF16 ? 2 : 1));
+    L.off_v = sec;
+    L.off_ks = 2 * sec;
+    L.off_vs = L.off_ks + (kv.dtype == BITQ_KV_INT8 ? align256(rows * 4) : 0);
+    L.total = L.off_vs + (kv.dtype == BITQ_KV_INT8 ? align256(rows * 4) : 0);
+    return L;
+}
+
+// Byte layout of a plan buffer.
+struct KvPlanLayout {
+    size_t off_len, off_start, off_slot, off_req, off_pos, total;
+};
+inline KvPlanLayout kv_plan_layout(const bitq_kv_plan_desc& d) {
+    KvPlanLayout L{};
+    L.off_len = 256;
+    L.off_start = L.off_len + align256(4 * static_cast<size_t>(d.requests));
+    L.off_slot = L.off_start + align256(4 * (static_cast<size_t>(d.requests) + 1));
+    const size_t t = align256(4 * static_cast<size_t>(d.tokens));
+    L.off_req = L.off_slot + t;
+    L.off_pos = L.off_req + t;
+    L.total = L.off_pos + t;
+    return L;
+}
+
+// How a paged attention call is split over workgroups (bitq_attn.hip).
+constexpr int kAttnWaves = 4;                    // waves per workgroup
+constexpr int kAttnUnit = 32 * kAttnWaves;       // tokens a workgroup takes per pass
+constexpr int kAttnMaxSplitRequests = 4096;      // the split kernel keeps their prefix sums in LDS
+struct AttnPlan {
+    int Dp, group, tiles;  // padded row, query heads per key-value head, 16-head tiles of them
+    int items;             // requests x key-value heads x tiles
+    int grid;              // workgroups of the main kernel
+    bool split;            // tokens split over workgroups and joined by a second kernel
+    size_t off_part, ws_bytes;
+};
+AttnPlan attn_plan(const bitq_attn_desc& d);
+
+struct W8A8Plan {
+    int kernel;            // which kernel (bitq_w8a8.hip)
+    int splits;
+    size_t ws_bytes;
+};
+W8A8Plan w8a8_plan(const bitq_w8a8_desc& d);
+
+int launch_kv_plan(const bitq_kv_plan_desc& d, const int32_t* old_len, const int32_t* new_len, int32_t* ring,
+                   const int32_t* state, int32_t* table, void* plan, void* stream);
+int launch_kv_write(const bitq_kvdesc& kv, const void* k, const void* v, int x_dtype, int64_t ks, int64_t vs,
+                    const int32_t* slots, int tokens, void* cache, void* stream);
+int launch_paged_attn(const bitq_attn_desc& d, const AttnPlan& plan, const void* q, int64_t q_stride,
+                      const void* cache, const int32_t* table, const int32_t* lens, void* out, float* lse, void* ws,
+                      void* stream);
+int launch_block_norm(const bitq_norm_desc& d, const void* u, const void* r, const void* post, const void* gate,
+                      const void* pre, void* ro, void* h, float* dscale, void* stream);
+int launch_gemm_w8a8(const bitq_w8a8_desc& d, const W8A8Plan& plan, const void* a, const float* sa, const void* w,
+                     const float* sw, void* y, void* ws, void* stream);
 
 // Device check (bitq_act.hip): is the current device a gfx950?
 int current_device_is_gfx950(int* is_gfx950);
