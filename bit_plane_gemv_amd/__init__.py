@@ -187,10 +187,25 @@ def _ptr(x) -> int | None:
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
+def _current_stream() -> int:
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+# The current stream's handle straight from torch's C module where this torch
+# has it (0.2 us against 2.9 us for building a Stream object on every call).
+if _torch is not None and hasattr(_torch._C, "_cuda_getCurrentRawStream") and hasattr(_torch._C, "_cuda_getDevice"):
+    def _raw_stream() -> int:
+        if not _torch.cuda.is_initialized():
+            return _current_stream()
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+else:
+    _raw_stream = _current_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream()
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)

@@ -227,8 +227,9 @@ typedef struct {
     uint32_t flags;   /* 0, or BITQ_F_ACC_INT32: y receives the int32 sums */
 } bitq_w8a8_desc;
 
-/* Workspace of bitq_gemm_w8a8 (0: none needed); as bitq_workspace_size the
- * caller zero-fills it once and every completed call leaves it zero. */
+/* Workspace of bitq_gemm_w8a8: the partial sums of calls whose k range is
+ * split over workgroups (0: none needed).  Its contents need no clearing and
+ * carry nothing from call to call; calls that share it must be ordered. */
 bitq_status bitq_w8a8_workspace(const bitq_w8a8_desc* desc, size_t* bytes);
 
 /*

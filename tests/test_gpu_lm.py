@@ -526,7 +526,9 @@ def int_product(a, w):
 
 W8A8 = [(1, 1, 16), (1, 16, 64), (1, 17, 4096), (2, 100, 80), (16, 33, 144), (17, 64, 1040), (33, 130, 272), (48, 40, 2064),
         (64, 300, 512), (49, 4096, 1024), (65, 129, 128), (100, 257, 400), (128, 128, 128), (129, 300, 1040), (200, 512, 4096),
-        (257, 1000, 656), (300, 16, 16), (1000, 777, 2000), (513, 2049, 272), (5, 20, 131056), (130, 140, 131056)]
+        (257, 1000, 656), (300, 16, 16), (1000, 777, 2000), (513, 2049, 272), (5, 20, 131056), (130, 140, 131056),
+        (9, 3000, 1040), (16, 9001, 272), (20, 7000, 528), (64, 300, 6160), (70, 1500, 7008), (520, 8100, 208), (3000, 9100, 80),
+        (2500, 3000, 336), (64, 64, 6400)]
 
 
 @pytest.mark.parametrize("M,N,K", W8A8)
@@ -549,7 +551,7 @@ def test_w8a8(M, N, K):
         got = y.cpu()
         assert torch.equal(got[:, :N].to(torch.int64), want), f"sums differ, first {(got[:, :N] != want).nonzero()[0].tolist()}"
         assert bool((got[:, N:] == 77).all()), "wrote past a row"
-        assert int(ws.count_nonzero()) == 0
+        ws.fill_(0x5A)                            # what an earlier call left does not matter
     exact = want.double() * sa.double()[:, None] * sw.double()
     for dt, t, tol in ((bq.DT_F32, torch.float32, 2.0 ** -22), (bq.DT_BF16, torch.bfloat16, BF16_ULP)):
         y = torch.full((M, ldy), 77, dtype=t, device="cuda")
