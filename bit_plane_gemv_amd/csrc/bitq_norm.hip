@@ -29,33 +29,50 @@ struct NormArgs {
     bool vec;  // every row chunk of 8 is 16-byte aligned, and C a multiple of 8
 };
 
-__device__ __forceinline__ void norm_load(const void* p, int dt, int64_t i, int n, bool vec, float (&v)[8]) {
-    if (dt == BITQ_DT_F32) {
-        const float* f = static_cast<const float*>(p) + i;
-        if (vec) {
-            const float4 a = reinterpret_cast<const float4*>(f)[0], b = reinterpret_cast<const float4*>(f)[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
+// 8 elements of a row as loaded (4 registers in bf16, 8 in fp32), converted
+// where they are used: a row then stays in few enough registers for four or
+// more rows per CU.
+template <int DT>
+struct Chunk {
+    uint4 a[DT == BITQ_DT_F32 ? 2 : 1];
+    __device__ __forceinline__ float operator[](int e) const {
+        const uint4 q = a[DT == BITQ_DT_F32 ? e >> 2 : 0];
+        const int w = DT == BITQ_DT_F32 ? e & 3 : e >> 1;
+        const uint32_t u = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
+        if (DT == BITQ_DT_F32) return __uint_as_float(u);
+        return __uint_as_float((e & 1) ? u & 0xFFFF0000u : u << 16);
+    }
+    // elements i .. i + 7 of p, the first n of them present (the rest 0)
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n, bool vec) {
+        if (DT == BITQ_DT_F32) {
+            const float* f = static_cast<const float*>(p) + i;
+            if (vec) {
+                a[0] = reinterpret_cast<const uint4*>(f)[0];
+                a[DT == BITQ_DT_F32 ? 1 : 0] = reinterpret_cast<const uint4*>(f)[1];
+            } else {
+                uint32_t u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < n ? f[e] : 0.0f;
-        }
-    } else {
-        const uint16_t* f = static_cast<const uint16_t*>(p) + i;
-        if (vec) {
-            const uint4 a = *reinterpret_cast<const uint4*>(f);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(w[e] << 16);
-                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                for (int e = 0; e < 8; ++e) u[e] = e < n ? __float_as_uint(f[e]) : 0u;
+                a[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                a[DT == BITQ_DT_F32 ? 1 : 0] = make_uint4(u[4], u[5], u[6], u[7]);
             }
         } else {
+            const uint16_t* f = static_cast<const uint16_t*>(p) + i;
+            if (vec) {
+                a[0] = *reinterpret_cast<const uint4*>(f);
+            } else {
+                uint32_t u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < n ? bf16_to_f32(f[e]) : 0.0f;
+                for (int e = 0; e < 8; ++e) u[e] = e < n ? f[e] : 0u;
+                a[0] = make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+            }
         }
     }
-}
+    __device__ __forceinline__ void zero() {
+        a[0] = make_uint4(0, 0, 0, 0);
+        a[DT == BITQ_DT_F32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+    }
+};
 
 __device__ __forceinline__ uint16_t norm_bf16(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
 __device__ __forceinline__ uint32_t norm_bf16x2(float a, float b) {
@@ -111,9 +128,8 @@ __device__ __forceinline__ float row_reduce(float v, float* s) {
         const float t = __shfl_xor(v, o, 64);
         v = MAX ? fmaxf(v, t) : v + t;
     }
-    if constexpr (W > 1) {
+    if constexpr (W > 1) {  // (s: a place that no wave can still be reading)
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        __syncthreads();  // (reads of the previous reduction are done)
         if (lane == 0) s[wave] = v;
         __syncthreads();
         v = s[0];
@@ -123,100 +139,131 @@ __device__ __forceinline__ float row_reduce(float v, float* s) {
     return v;
 }
 
-template <int W, int NV>
+template <int W, int NV, int UDT, int RDT, int WDT>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormArgs a) {
     constexpr int T = 64 * W;                // lanes of a row
     constexpr int RPB = W == 1 ? 4 : 1;      // rows of a workgroup
-    __shared__ float s_red[W];
+    // rows of 64 chunks and more per lane-group would not fit the registers
+    // with r and the gate held from the start: these are then read late
+    constexpr bool EARLY = NV * W < 64;
+    // a place for each reduction of a row, for two rows in turn: a row has at
+    // least one barrier, so no wave is more than a row behind
+    __shared__ float s_red[2][3][W];
     const int ln = W == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int sub = W == 1 ? threadIdx.x >> 6 : 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + sub; row < a.M; row += static_cast<int64_t>(gridDim.x) * RPB) {
-        float u[NV][8], r[NV][8], g[NV][8], po[NV][8], pr[NV][8];
+    int turn = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + sub; row < a.M;
+         row += static_cast<int64_t>(gridDim.x) * RPB, turn ^= 1) {
+        Chunk<UDT> u[NV];
+        Chunk<RDT> r[EARLY ? NV : 1];
+        Chunk<WDT> g[EARLY ? NV : 1], po[1], pr[1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = 8 * (ln + T * j), n = min(8, a.C - i);  // elements of this chunk (<= 0: none)
             const bool vec = a.vec && n == 8;
-            if (n > 0) {
-                norm_load(a.u, a.udt, row * a.us + i, n, vec, u[j]);
-                if (a.r) norm_load(a.r, a.rdt, row * a.rs + i, n, vec, r[j]);
-                if (a.gate) norm_load(a.gate, a.wdt, row * a.gs + i, n, vec, g[j]);
-                if (a.post) norm_load(a.post, a.wdt, i, n, vec, po[j]);
-                if (a.pre) norm_load(a.pre, a.wdt, i, n, vec, pr[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[j][e] = r[j][e] = g[j][e] = po[j][e] = pr[j][e] = 0.0f;
+            u[j].zero();
+            if (n <= 0) continue;
+            u[j].load(a.u, row * a.us + i, n, vec);
+            if constexpr (EARLY) {
+                if (a.r) r[j].load(a.r, row * a.rs + i, n, vec);
+                if (a.gate) g[j].load(a.gate, row * a.gs + i, n, vec);
+            }
+            if constexpr (NV == 1) {
+                if (a.post) po[0].load(a.post, i, n, vec);
+                if (a.pre) pr[0].load(a.pre, i, n, vec);
             }
         }
+        float s = a.branch;
         if (a.post) {
             float q = 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) q = fmaf(u[j][e], u[j][e], q);
-            q = row_reduce<W, false>(q, s_red);
-            const float s = 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_post);
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[j][e] = u[j][e] * s * po[j][e];
+            q = row_reduce<W, false>(q, s_red[turn][0]);
+            s *= 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_post);
         }
-        float q = 0.0f;
+        float y[NV][8], q = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const int i = 8 * (ln + T * j), n = min(8, a.C - i);
+            const bool vec = a.vec && n == 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float y = a.branch * u[j][e];
-                if (a.gate) y *= g[j][e];
-                if (a.r) y = fmaf(a.res, r[j][e], y);
-                u[j][e] = y;
-                q = fmaf(y, y, q);
+            for (int e = 0; e < 8; ++e) y[j][e] = u[j][e] * s;
+            if (n > 0) {
+                constexpr int one = 0;
+                if (a.post) {
+                    if constexpr (NV > 1) po[0].load(a.post, i, n, vec);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[j][e] *= po[0][e];
+                }
+                if (a.gate) {
+                    const int k = EARLY ? j : one;
+                    if constexpr (!EARLY) g[0].load(a.gate, row * a.gs + i, n, vec);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[j][e] *= g[k][e];
+                }
+                if (a.r) {
+                    const int k = EARLY ? j : one;
+                    if constexpr (!EARLY) r[0].load(a.r, row * a.rs + i, n, vec);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[j][e] = fmaf(a.res, r[k][e], y[j][e]);
+                }
+                if (a.ro) norm_store(a.ro, RDT, row * a.ros + i, n, vec, y[j]);
             }
-        if (a.ro) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(y[j][e], y[j][e], q);
+        }
+        if (a.pre) {
+            q = row_reduce<W, false>(q, s_red[turn][1]);
+            const float f = 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_pre);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = 8 * (ln + T * j), n = min(8, a.C - i);
-                if (n > 0) norm_store(a.ro, a.rdt, row * a.ros + i, n, a.vec && n == 8, u[j]);
+                if (n <= 0) continue;
+                if constexpr (NV > 1) pr[0].load(a.pre, i, n, a.vec && n == 8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[j][e] = y[j][e] * f * pr[0][e];
             }
-        }
-        if (a.pre) {
-            q = row_reduce<W, false>(q, s_red);
-            const float s = 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_pre);
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[j][e] = u[j][e] * s * pr[j][e];
         }
         if (a.odt == BITQ_DT_ROW8) {  // the arithmetic of the activation quantizer
             float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(u[j][e]));
-            m = row_reduce<W, true>(m, s_red);
-            const float s = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[j][e]));
+            m = row_reduce<W, true>(m, s_red[turn][2]);
+            const float f = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
             if (ln == 0) a.d[row] = m > 0.0f ? __fdiv_rn(m, 127.0f) : 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    u[j][e] = fminf(fmaxf(rintf(__fmul_rn(u[j][e], s)), -127.0f), 127.0f);
+                for (int e = 0; e < 8; ++e) y[j][e] = fminf(fmaxf(rintf(__fmul_rn(y[j][e], f)), -127.0f), 127.0f);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = 8 * (ln + T * j), n = min(8, a.C - i);
-            if (n > 0) norm_store(a.h, a.odt, row * a.hs + i, n, a.vec && n == 8, u[j]);
+            if (n > 0) norm_store(a.h, a.odt, row * a.hs + i, n, a.vec && n == 8, y[j]);
         }
     }
 }
 
-template <int W>
-static void launch_norm(const NormArgs& a, int nv, hipStream_t st) {
+template <int W, int NV>
+static void launch_norm(const NormArgs& a, hipStream_t st) {
     constexpr int rpb = W == 1 ? 4 : 1;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((a.M + rpb - 1) / rpb, 1 << 16)));
     const dim3 block(W == 1 ? 256 : 64 * W);
-    if (nv <= 1) hipLaunchKernelGGL((block_norm_kernel<W, 1>), grid, block, 0, st, a);
-    else if (nv <= 2) hipLaunchKernelGGL((block_norm_kernel<W, 2>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((block_norm_kernel<W, 4>), grid, block, 0, st, a);
+    constexpr int F = BITQ_DT_F32, B = BITQ_DT_BF16;
+    switch ((a.udt == B) * 4 + (a.rdt == B) * 2 + (a.wdt == B)) {
+        case 0: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, F, F>), grid, block, 0, st, a); break;
+        case 1: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, F, B>), grid, block, 0, st, a); break;
+        case 2: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, B, F>), grid, block, 0, st, a); break;
+        case 3: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, B, B>), grid, block, 0, st, a); break;
+        case 4: hipLaunchKernelGGL((block_norm_kernel<W, NV, B, F, F>), grid, block, 0, st, a); break;
+        case 5: hipLaunchKernelGGL((block_norm_kernel<W, NV, B, F, B>), grid, block, 0, st, a); break;
+        case 6: hipLaunchKernelGGL((block_norm_kernel<W, NV, B, B, F>), grid, block, 0, st, a); break;
+        default: hipLaunchKernelGGL((block_norm_kernel<W, NV, B, B, B>), grid, block, 0, st, a); break;
+    }
 }
 
 int launch_block_norm(const bitq_norm_desc& d, const void* u, const void* r, const void* post, const void* gate,
@@ -234,20 +281,19 @@ int launch_block_norm(const bitq_norm_desc& d, const void* u, const void* r, con
             ok(post, d.w_dtype, 0) && ok(pre, d.w_dtype, 0) && ok(gate, d.w_dtype, d.gate_stride) &&
             ok(h, d.out_dtype, d.h_stride);
     const int chunks = (d.width + 7) / 8;
-    // many rows: the fewest waves that hold a row with 4 chunks a lane; few
-    // rows: one chunk a lane, for the shortest chain
-    const int per = d.rows >= 1024 ? 4 : 1;
-    int W = 1;
-    while (W < 16 && 64 * W * per < chunks) W *= 2;
-    const int nv = (chunks + 64 * W - 1) / (64 * W);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    switch (W) {
-        case 1: launch_norm<1>(a, nv, st); break;
-        case 2: launch_norm<2>(a, nv, st); break;
-        case 4: launch_norm<4>(a, nv, st); break;
-        case 8: launch_norm<8>(a, nv, st); break;
-        default: launch_norm<16>(a, nv, st); break;
-    }
+    // many rows: the fewest waves that hold a row; few rows: one chunk a
+    // lane, for the shortest chain
+    const bool many = d.rows >= 1024;
+    if (chunks <= 64) launch_norm<1, 1>(a, st);
+    else if (many && chunks <= 128) launch_norm<1, 2>(a, st);
+    else if (many && chunks <= 256) launch_norm<1, 4>(a, st);
+    else if (chunks <= 256) launch_norm<4, 1>(a, st);
+    else if (many && chunks <= 512) launch_norm<4, 2>(a, st);
+    else if (many && chunks <= 1024) launch_norm<4, 4>(a, st);
+    else if (chunks <= 1024) launch_norm<16, 1>(a, st);
+    else if (chunks <= 2048) launch_norm<16, 2>(a, st);
+    else launch_norm<16, 4>(a, st);
     return static_cast<int>(hipGetLastError());
 }
 
