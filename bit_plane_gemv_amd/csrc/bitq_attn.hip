@@ -51,7 +51,6 @@ struct AttnArgs {
     int R, H, A, group, tiles, D, page_shift, pages, table_stride, max_len, window;
     float c;           // scale log2(e): p = 2^(c s - m)
     int qdt, odt;
-    bool qvec;         // 8-element chunks of q are 16-byte aligned
 };
 
 // Tokens [lo, hi) of request r.
@@ -64,6 +63,8 @@ __device__ __forceinline__ int token_units(int lo, int hi) {
     return hi > lo ? (hi - (lo & ~31) + kAttnUnit - 1) / kAttnUnit : 0;
 }
 
+// (2^x by the hardware instruction: 1 ulp, results below 2^-126 flushed to 0)
+//
 // Maximum / sum over the four lanes 16 g + j of a column.
 __device__ __forceinline__ float col_max(float v) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -93,6 +94,18 @@ __device__ __forceinline__ void split_terms(const float (&x)[8], bf16x8_t (&t)[N
         }
 }
 
+// Place of element d of a query head in the operands of S = K q^T: chunk c,
+// lane group g, position e.  bf16 rows: d = 32 c + 8 g + e.  int8 rows: a
+// lane's 16-byte load covers two chunks, d = 64 (c / 2) + 16 g + 8 (c % 2) + e
+// (a last odd chunk as for bf16).
+template <bool I8, int NC>
+__device__ __forceinline__ int q_place(int d, int head) {
+    const bool pair = I8 && d < 64 * (NC / 2);
+    const int c = pair ? 2 * (d >> 6) + ((d >> 3) & 1) : d >> 5;
+    const int g = pair ? (d >> 4) & 3 : (d >> 3) & 3;
+    return ((c * 64) + 16 * g + head) * 8 + (d & 7);
+}
+
 // 8 int8 codes as bf16 (exact)
 __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t lo, uint32_t hi) {
     bf16x8_t v;
@@ -116,62 +129,30 @@ template <int KVT, int NC, bool HI>
 struct AttnWave {
     static constexpr int NQ = HI ? 3 : 1, NP = HI ? 3 : 2, Dp = 32 * NC;
     static constexpr bool I8 = KVT == BITQ_KV_INT8;
-    bf16x8_t q[NQ][NC];
+    bf16x8_t q[HI ? 1 : NC];  // bf16 q: the operands; else they are read from LDS where they are used
     f32x4_t o[2 * NC];
     float m, l;
     const AttnArgs& a;
     const int lane, g, j;
+    const __bf16* sq;    // the query tile's operands in LDS: [NQ][NC][64 lanes][8]
     const int32_t* row;  // the request's row of the table
     int h, lo, hi;
 
-    __device__ __forceinline__ AttnWave(const AttnArgs& args, int ln)
-        : a(args), lane(ln), g(ln >> 4), j(ln & 15) {}
+    __device__ __forceinline__ AttnWave(const AttnArgs& args, int ln, const __bf16* s)
+        : a(args), lane(ln), g(ln >> 4), j(ln & 15), sq(s) {}
 
-    // Element of the row at which lane group g's k positions of chunk c begin.
-    // bf16: 32 c + 8 g.  int8: a lane's 16-byte load covers two chunks.
-    static __device__ __forceinline__ int chunk_elem(int c, int g) {
-        if (I8 && (c | 1) < NC) return 64 * (c >> 1) + 16 * g + 8 * (c & 1);
-        return 32 * c + 8 * g;
+    __device__ __forceinline__ bf16x8_t q_operand(int n, int c) const {
+        return *reinterpret_cast<const bf16x8_t*>(sq + ((n * NC + c) * 64 + lane) * 8);
     }
 
-    __device__ __forceinline__ void begin(int r, int hk, int tile, int lo_, int hi_) {
+    __device__ __forceinline__ void begin(int r, int hk, int lo_, int hi_) {
         h = hk;
         lo = lo_;
         hi = hi_;
         row = a.table + static_cast<size_t>(r) * a.table_stride;
-        const int head = 16 * tile + j;
-        const bool live = head < a.group;
-        const int64_t at = static_cast<int64_t>(r) * a.q_stride + (static_cast<int64_t>(hk) * a.group + (live ? head : 0)) * a.D;
+        if constexpr (!HI) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int d = chunk_elem(c, g);
-            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (live && d < a.D) {
-                if (a.qvec) {  // (D is a multiple of 8 then)
-                    if (a.qdt == BITQ_DT_F32) {
-                        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + d);
-                        const float4 u = p[0], w = p[1];
-                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-                        x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
-                    } else {
-                        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[2 * e] = __uint_as_float(w[e] << 16);
-                            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (d + e < a.D) x[e] = load_act(a.q, a.qdt, static_cast<size_t>(at + d + e));
-                }
-            }
-            bf16x8_t t[NQ];
-            split_terms<NQ>(x, t);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) q[n][c] = t[n];
+            for (int c = 0; c < NC; ++c) q[c] = q_operand(0, c);
         }
 #pragma unroll
         for (int c = 0; c < 2 * NC; ++c) o[c] = f32x4_t{0, 0, 0, 0};
@@ -195,23 +176,22 @@ struct AttnWave {
         for (int i = 0; i < 3; ++i) pg[i] = row[tok[i] >> a.page_shift];
     }
 
-    __device__ __forceinline__ void load(int s, const int (&pg)[3], AttnStep<KVT, NC>& L) const {
+    // Row of the pool of token tok, whose page is pg.
+    __device__ __forceinline__ size_t pool_row(int tok, int pg) const {
+        const uint32_t p = static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.pages) ? pg : 0;
+        return ((static_cast<size_t>(p) * a.H + h) << a.page_shift) + (tok & ((1 << a.page_shift) - 1));
+    }
+    __device__ __forceinline__ void load_k(int s, const int (&pg)[3], AttnStep<KVT, NC>& L) const {
         constexpr int es = I8 ? 1 : 2;
         int tok[3];
         tokens(s, tok);
-        const int P = 1 << a.page_shift;
-        size_t at[3];  // row of the pool
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int p = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.pages) ? pg[i] : 0;
-            at[i] = ((static_cast<size_t>(p) * a.H + h) << a.page_shift) + (tok[i] & (P - 1));
-        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint8_t* kp = a.cache + at[t] * (Dp * es);
+            const uint8_t* kp = a.cache + pool_row(tok[t], pg[t]) * (Dp * es);
             if constexpr (!I8) {
+                kp += 16 * g;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) L.k[t][c] = *reinterpret_cast<const uint4*>(kp + 64 * c + 16 * g);
+                for (int c = 0; c < NC; ++c) L.k[t][c] = *reinterpret_cast<const uint4*>(kp + 64 * c);
             } else {
 #pragma unroll
                 for (int c = 0; c < NC / 2; ++c) L.k[t][c] = *reinterpret_cast<const uint4*>(kp + 64 * c + 16 * g);
@@ -221,25 +201,31 @@ struct AttnWave {
                 }
             }
         }
-        const uint8_t* vp = a.cache + a.off_v + at[2] * (Dp * es);  // (groups of 8 rows: at[2] is a multiple of 8)
-        if constexpr (!I8) {
+        if constexpr (I8) {
+            const float4* p = reinterpret_cast<const float4*>(a.cache + a.off_ks) + pool_row(tok[2], pg[2]) / 4;
+            L.ks[0] = p[0];
+            L.ks[1] = p[1];
+        }
+    }
+    __device__ __forceinline__ void load_v(int s, const int (&pg)[3], AttnStep<KVT, NC>& L) const {
+        constexpr int es = I8 ? 1 : 2;
+        int tok[3];
+        tokens(s, tok);
+        const size_t at = pool_row(tok[2], pg[2]);  // (a multiple of 8: groups of 8 rows)
+        const uint8_t* vp = a.cache + a.off_v + at * (Dp * es) + 16 * j;
+        // bf16: 16 bytes are element 16 c + j of 8 tokens; int8: elements 32 c + 2 j and 32 c + 2 j + 1
 #pragma unroll
-            for (int c = 0; c < 2 * NC; ++c) L.v[c] = *reinterpret_cast<const uint4*>(vp + 256 * c + 16 * j);
-        } else {
-            // 16 bytes: elements 32 c + 2 j and 32 c + 2 j + 1 of 8 tokens
-#pragma unroll
-            for (int c = 0; c < NC; ++c) L.v[c] = *reinterpret_cast<const uint4*>(vp + 256 * c + 16 * j);
-            const float4* ksp = reinterpret_cast<const float4*>(a.cache + a.off_ks) + at[2] / 4;
-            const float4* vsp = reinterpret_cast<const float4*>(a.cache + a.off_vs) + at[2] / 4;
-            L.ks[0] = ksp[0];
-            L.ks[1] = ksp[1];
-            L.vs[0] = vsp[0];
-            L.vs[1] = vsp[1];
+        for (int c = 0; c < (I8 ? NC : 2 * NC); ++c) L.v[c] = *reinterpret_cast<const uint4*>(vp + 256 * c);
+        if constexpr (I8) {
+            const float4* p = reinterpret_cast<const float4*>(a.cache + a.off_vs) + at / 4;
+            L.vs[0] = p[0];
+            L.vs[1] = p[1];
         }
     }
 
-    __device__ __forceinline__ void compute(int s, const AttnStep<KVT, NC>& L) {
-        float x[8];
+    // Scores of tokens s + 8 g + e, scaled to powers of two; masked ones are
+    // -inf.  keep: bit e is set if the token is in [lo, hi).
+    __device__ __forceinline__ void scores(int s, const AttnStep<KVT, NC>& L, float (&x)[8], uint32_t& keep, bool edge) const {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4_t acc = {0, 0, 0, 0};
@@ -254,69 +240,82 @@ struct AttnWave {
                 }
 #pragma unroll
                 for (int n = NQ - 1; n >= 0; --n)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][c], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, HI ? q_operand(n, c) : q[HI ? 0 : c], acc, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[4 * t + i] = acc[i];
         }
-        // scores of tokens s + 8 g + e; masked ones become -inf
-        const bool edge = s < lo || s + 32 > hi;  // (the same for the whole wave)
         if constexpr (I8) {
             const float ks[8] = {L.ks[0].x, L.ks[0].y, L.ks[0].z, L.ks[0].w, L.ks[1].x, L.ks[1].y, L.ks[1].z, L.ks[1].w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= ks[e];
         }
-        uint32_t keep = 0xFFu;  // bit e: token s + 8 g + e is in [lo, hi)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= a.c;
+        keep = 0xFFu;
         if (edge) {
+            asm volatile("");  // (a branch, not selects in every step)
             keep = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int tk = s + 8 * g + e;
-                if (tk >= lo && tk < hi) keep |= 1u << e;
+                const bool in = tk >= lo && tk < hi;
+                keep |= in ? 1u << e : 0u;
+                x[e] = in ? x[e] : -INFINITY;
             }
         }
+    }
+
+    // The weights p of those scores (in x), with m, l and O rescaled if m grows.
+    __device__ __forceinline__ void weights(float (&x)[8]) {
         float mx = -FLT_MAX;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= a.c;
-            if (edge && !(keep & (1u << e))) x[e] = -INFINITY;
-            mx = fmaxf(mx, x[e]);
-        }
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, x[e]);
         mx = col_max(mx);
         if (__any(mx > m)) {
             const float mn = fmaxf(m, mx);
-            const float f = exp2f(m - mn);
+            const float f = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= f;
 #pragma unroll
             for (int c = 0; c < 2 * NC; ++c) o[c] *= f;
         }
-        float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = exp2f(x[e] - m);
-            l += p[e];
+            x[e] = __builtin_amdgcn_exp2f(x[e] - m);
+            l += x[e];
         }
+    }
+
+    __device__ __forceinline__ void values(AttnStep<KVT, NC>& L, float (&p)[8], uint32_t keep, bool edge) {
         if constexpr (I8) {
-            const float vs[8] = {L.vs[0].x, L.vs[0].y, L.vs[0].z, L.vs[0].w, L.vs[1].x, L.vs[1].y, L.vs[1].z, L.vs[1].w};
+            float vs[8] = {L.vs[0].x, L.vs[0].y, L.vs[0].z, L.vs[0].w, L.vs[1].x, L.vs[1].y, L.vs[1].z, L.vs[1].w};
+            if (edge) {  // scales in masked places may be infinite or NaN
+                asm volatile("");
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = (edge && !(keep & (1u << e))) ? 0.0f : p[e] * vs[e];
+                for (int e = 0; e < 8; ++e) vs[e] = keep & (1u << e) ? vs[e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] *= vs[e];
         }
         bf16x8_t pf[NP];
         split_terms<NP>(p, pf);
+        if (!I8 && edge) {  // what lies in masked places may be infinite or NaN: 0 p must stay 0
+            asm volatile("");
+            uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e >> 1] &= keep & (1u << e) ? ~0u : (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+            for (int c = 0; c < 2 * NC; ++c) {
+                uint4& u = L.v[I8 ? 0 : c];
+                u = make_uint4(u.x & w[0], u.y & w[1], u.z & w[2], u.w & w[3]);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 2 * NC; ++c) {
             bf16x8_t vf;
             if constexpr (!I8) {
-                uint4 u = L.v[c];
-                if (edge) {  // what lies in masked places may be infinite or NaN: 0 p must stay 0
-                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!(keep & (1u << e))) w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-                    u = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                vf = __builtin_bit_cast(bf16x8_t, u);
+                vf = __builtin_bit_cast(bf16x8_t, L.v[c]);
             } else {
                 const uint4 u = L.v[c >> 1];  // (int8 codes are finite whatever the bytes)
                 vf = (c & 1) ? codes_bf16(u.z, u.w) : codes_bf16(u.x, u.y);
@@ -327,16 +326,38 @@ struct AttnWave {
         }
     }
 
-    // The wave's steps s0, s0 + stride, ... below s1, loads one step ahead.
+    // The wave's steps s0, s0 + stride, ... below s1.  A step's registers are
+    // loaded again as soon as they are free: the next keys are in flight
+    // while the weights and values are worked on, the next values while the
+    // next scores are.  (The loads are unconditional, the last step's are
+    // repeated: behind a branch the compiler would wait for all of them.  A
+    // second set of registers, or the first loads issued before the queries
+    // are staged, measured no better.)
+    __device__ __forceinline__ void step(int s, int next, int after, AttnStep<KVT, NC>& L, int (&pg)[3]) {
+        const bool edge = s < lo || s + 32 > hi;  // (the same for the whole wave)
+        float x[8];
+        uint32_t keep;
+        asm volatile("" ::: "memory");  // (q's operands are read again, not kept in registers)
+        scores(s, L, x, keep, edge);
+        load_k(next, pg, L);
+        weights(x);
+        values(L, x, keep, edge);
+        load_v(next, pg, L);
+        lookup(after, pg);
+    }
     __device__ __forceinline__ void run(int s0, int s1, int stride) {
         if (s0 >= s1) return;
-        AttnStep<KVT, NC> A;
+        AttnStep<KVT, NC> L;
         int pg[3];
+        auto upto = [&](int s) { return s < s1 ? s : s0; };
         lookup(s0, pg);
-        for (int s = s0; s < s1; s += stride) {
-            load(s, pg, A);
-            if (s + stride < s1) lookup(s + stride, pg);
-            compute(s, A);
+        load_k(s0, pg, L);
+        load_v(s0, pg, L);
+        lookup(upto(s0 + stride), pg);
+        for (int s = s0;;) {
+            step(s, upto(s + stride), upto(s + 2 * stride), L, pg);
+            s += stride;
+            if (s >= s1) return;
         }
     }
 
@@ -372,7 +393,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // First index i in [0, n) with a[i] > x (n if none); a ascending.
-__device__ __forceinline__ int first_above64(const int32_t* a, int n, int64_t x) {
+__device__ __forceinline__ int first_above32(const int32_t* a, int n, int x) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -391,18 +412,20 @@ __device__ __forceinline__ int first_above64(const int32_t* a, int n, int64_t x)
 // that lies in several ranges go to the workgroup's two partial results (slot
 // 0: an item begun elsewhere, slot 1: one begun here) for the join kernel.
 template <int KVT, int NC, bool HI, bool SPLIT>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void paged_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) void paged_attn_kernel(AttnArgs a) {
     constexpr int Dp = 32 * NC, W = kAttnWaves, ROW = Dp + 4;
     __shared__ __align__(16) float s_o[W][16 * ROW];
     __shared__ float s_m[W][16], s_l[W][16];
+    constexpr int NQ = HI ? 3 : 1;
+    __shared__ __align__(16) __bf16 s_q[NQ * 16 * Dp];
     extern __shared__ int32_t s_pre[];  // SPLIT: [R + 1]
     __shared__ int32_t s_scan[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int HT = a.H * a.tiles;
-    AttnWave<KVT, NC, HI> w(a, lane);
+    AttnWave<KVT, NC, HI> w(a, lane, s_q);
 
-    int64_t x = blockIdx.x, x1 = static_cast<int64_t>(blockIdx.x) + 1;  // units (SPLIT) or the item
-    int64_t U = 1;
+    int x = blockIdx.x, x1 = x + 1;  // units (SPLIT; fewer than 2^31) or the item
+    int U = 1;
     if constexpr (SPLIT) {
         int carry = 0;
         for (int r0 = 0; r0 < a.R; r0 += 64 * W) {
@@ -434,48 +457,59 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void paged_attn_kernel(AttnArgs
         __syncthreads();
         if (blockIdx.x == 0)
             for (int r = tid; r <= a.R; r += 64 * W) a.prefix[r] = s_pre[r];
-        U = s_pre[a.R];
-        const int64_t T = U * HT;
+        U = wave_uniform(s_pre[a.R]);
+        const int64_t T = static_cast<int64_t>(U) * HT;
         // (with fewer units than workgroups the surplus workgroups have none:
         // every range below G is non-empty, which the join relies on)
         const int64_t G = min(T, static_cast<int64_t>(gridDim.x));
         if (blockIdx.x >= G) return;
-        x = T * blockIdx.x / G;
-        x1 = T * (static_cast<int64_t>(blockIdx.x) + 1) / G;
+        x = static_cast<int>(T * blockIdx.x / G);
+        x1 = static_cast<int>(T * (static_cast<int64_t>(blockIdx.x) + 1) / G);
     }
     while (x < x1) {
         int ht, r, lo, hi, s0, s1;
         bool whole = true;
-        int slot = 0;
-        int64_t next = x + 1;
+        int slot = 0, next = x + 1;
         if constexpr (SPLIT) {
-            ht = static_cast<int>(x / U);
-            const int64_t rem = x - ht * U;
-            r = first_above64(s_pre + 1, a.R, rem);
+            ht = x / U;
+            const int rem = x - ht * U;
+            r = wave_uniform(first_above32(s_pre + 1, a.R, rem));
             token_range(a, r, lo, hi);
-            const int64_t end = ht * U + s_pre[r + 1];
+            const int end = ht * U + wave_uniform(s_pre[r + 1]);
             next = min(x1, end);
-            const int64_t k0 = rem - s_pre[r];
+            const int k0 = rem - wave_uniform(s_pre[r]);
             whole = k0 == 0 && next == end;
             slot = k0 == 0 ? 1 : 0;
-            s0 = (lo & ~31) + static_cast<int>(k0) * kAttnUnit;
-            s1 = static_cast<int>(min(static_cast<int64_t>(hi), s0 + (next - x) * kAttnUnit));
+            s0 = (lo & ~31) + k0 * kAttnUnit;
+            s1 = min(hi, s0 + (next - x) * kAttnUnit);
         } else {
-            ht = static_cast<int>(x % HT);
-            r = static_cast<int>(x / HT);
+            ht = x % HT;
+            r = x / HT;
             token_range(a, r, lo, hi);
             s0 = lo & ~31;
             s1 = hi;
         }
         // (values that are the same for the whole wave, kept in scalar registers)
-        ht = wave_uniform(ht);
-        r = wave_uniform(r);
-        const int hk = ht / a.tiles, tile = ht - hk * a.tiles;
-        w.begin(r, hk, tile, wave_uniform(lo), wave_uniform(hi));
+        const int hk = ht / a.tiles, tile = ht - hk * a.tiles, heads = min(16, a.group - 16 * tile);
+        // ---- the tile's queries into LDS, as the terms and in the order of the operands
+        const int64_t qat = static_cast<int64_t>(r) * a.q_stride + (static_cast<int64_t>(hk) * a.group + 16 * tile) * a.D;
+        for (int i = tid; i < 16 * Dp; i += 64 * W) {
+            const int head = i / Dp, d = i - head * Dp;
+            float v = 0.0f;
+            if (head < heads && d < a.D) v = load_act(a.q, a.qdt, static_cast<size_t>(qat + head * a.D + d));
+            const int at = q_place<KVT == BITQ_KV_INT8, NC>(d, head);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const __bf16 b = static_cast<__bf16>(v);
+                s_q[n * (16 * Dp) + at] = b;
+                v -= static_cast<float>(b);
+            }
+        }
+        __syncthreads();
+        w.begin(r, hk, wave_uniform(lo), wave_uniform(hi));
         w.run(wave_uniform(s0) + 32 * wave, wave_uniform(s1), kAttnUnit);
         w.park(s_o[wave], s_m[wave], s_l[wave]);
         __syncthreads();
-        const int heads = min(16, a.group - 16 * tile);
         float* part = SPLIT ? a.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (16 * (Dp + 2)) : nullptr;
         for (int i = tid; i < heads * Dp; i += 64 * W) {
             const int head = i / Dp, d = i - head * Dp;
@@ -485,7 +519,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void paged_attn_kernel(AttnArgs
             float sum = 0.0f, acc = 0.0f;
 #pragma unroll
             for (int v = 0; v < W; ++v) {
-                const float f = exp2f(s_m[v][head] - M);
+                const float f = __builtin_amdgcn_exp2f(s_m[v][head] - M);
                 sum += f * s_l[v][head];
                 acc += f * s_o[v][head * ROW + d];
             }
@@ -533,7 +567,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void attn_join_kernel(Attn
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = lane + 64 * e < Dp ? p[head * Dp + lane + 64 * e] : 0.0f;
-            const float mn = fmaxf(M, pm), f = exp2f(M - mn), fp = exp2f(pm - mn);
+            const float mn = fmaxf(M, pm), f = __builtin_amdgcn_exp2f(M - mn), fp = __builtin_amdgcn_exp2f(pm - mn);
             M = mn;
             L = L * f + pl * fp;
 #pragma unroll
@@ -555,7 +589,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void attn_join_kernel(Attn
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
         for (int v = 0; v < NW; ++v) {
-            const float f = exp2f(s_m[v] - M);
+            const float f = __builtin_amdgcn_exp2f(s_m[v] - M);
             L += f * s_l[v];
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] += f * s_acc[v][lane + 64 * e];
@@ -629,8 +663,6 @@ int launch_paged_attn(const bitq_attn_desc& d, const AttnPlan& plan, const void*
     a.c = d.scale * 1.44269504088896340736f;
     a.qdt = d.q_dtype;
     a.odt = d.out_dtype;
-    const int per = d.q_dtype == BITQ_DT_F32 ? 4 : 8;
-    a.qvec = aligned(q, 16) && q_stride % per == 0 && d.kv.head_dim % 8 == 0;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
     if (d.kv.dtype == BITQ_KV_BF16) {

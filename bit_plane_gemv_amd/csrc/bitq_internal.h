@@ -193,6 +193,13 @@ inline KvPlanLayout kv_plan_layout(const bitq_kv_plan_desc& d) {
 constexpr int kAttnWaves = 4;                    // waves per workgroup
 constexpr int kAttnUnit = 32 * kAttnWaves;       // tokens a workgroup takes per pass
 constexpr int kAttnMaxSplitRequests = 4096;      // the split kernel keeps their prefix sums in LDS
+// Workgroups per CU that the registers of the kernel for rows of 32 nc
+// elements allow without spilling (hi: fp32 q or output).  Rows of 128 in
+// int8: 3 per CU measured 96 against 104 us with 2 (64 ragged requests).
+constexpr int attn_groups_per_cu(int kv_dtype, int nc, bool hi) {
+    const bool i8 = kv_dtype == BITQ_KV_INT8;
+    return nc <= 2 ? 4 : nc <= (i8 ? 4 : 3) ? 3 : nc <= (i8 ? (hi ? 6 : 7) : (hi ? 5 : 6)) ? 2 : 1;
+}
 struct AttnPlan {
     int Dp, group, tiles;  // padded row, query heads per key-value head, 16-head tiles of them
     int items;             // requests x key-value heads x tiles

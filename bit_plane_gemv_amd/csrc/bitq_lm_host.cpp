@@ -126,8 +126,12 @@ AttnPlan attn_plan(const bitq_attn_desc& d) {
     p.items = d.requests * d.kv.kv_heads * p.tiles;
     const int64_t span = d.window > 0 ? std::min<int64_t>(d.max_len, static_cast<int64_t>(d.window) + 31) : d.max_len;
     const int64_t units = (span + kAttnUnit - 1) / kAttnUnit;  // of the longest request
-    p.split = units > 1 && d.requests <= kAttnMaxSplitRequests;
-    p.grid = p.split ? static_cast<int>(std::min<int64_t>(512, p.items * units)) : p.items;
+    const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    p.split = units > 1 && d.requests <= kAttnMaxSplitRequests && p.items * units < INT32_MAX;
+    // (the CUs filled as often as registers allow; two units and more for a
+    // workgroup measured slower: one request of 2049 tokens 17.5 against 15.1 us)
+    const int64_t all = p.items * units, full = 256 * attn_groups_per_cu(d.kv.dtype, p.Dp / 32, hi);
+    p.grid = p.split ? static_cast<int>(std::min(full, all)) : p.items;
     if (p.split) {
         // prefix sums of the requests' units, then two partial results per workgroup: 16 heads x (Dp + 2) floats
         p.off_part = align256(4 * (static_cast<size_t>(d.requests) + 1));
