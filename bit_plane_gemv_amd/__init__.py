@@ -195,12 +195,27 @@ def _current_stream() -> int:
 # The current stream's handle straight from torch's C module where this torch
 # has it (0.2 us against 2.9 us for building a Stream object on every call).
 if _torch is not None and hasattr(_torch._C, "_cuda_getCurrentRawStream") and hasattr(_torch._C, "_cuda_getDevice"):
+    _raw_stream_of, _device, _started = _torch._C._cuda_getCurrentRawStream, _torch._C._cuda_getDevice, False
+
     def _raw_stream() -> int:
-        if not _torch.cuda.is_initialized():
-            return _current_stream()
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        global _started
+        if not _started:
+            if not _torch.cuda.is_initialized():
+                return _current_stream()
+            _started = True
+        return _raw_stream_of(_device())
 else:
     _raw_stream = _current_stream
+
+
+def _addr(x) -> int | None:
+    """_ptr for the calls of a decode step: tensors first."""
+    if x is None:
+        return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
 
 
 def _stream(stream) -> int | None:
@@ -464,7 +479,7 @@ def kv_plan_views(desc: KvPlanDesc, plan) -> dict:
 
 def kv_plan(desc: KvPlanDesc, old_len, new_len, ring, state, table, plan, stream=None):
     """One scheduling step: pages from and to the ring, tables, slots (bitq_kv_plan)."""
-    _check(_lib.bitq_kv_plan(desc, _ptr(old_len), _ptr(new_len), _ptr(ring), _ptr(state), _ptr(table), _ptr(plan),
+    _check(_lib.bitq_kv_plan(desc, _addr(old_len), _addr(new_len), _addr(ring), _addr(state), _addr(table), _addr(plan),
                              _nbytes(plan), _stream(stream)))
 
 
@@ -472,9 +487,9 @@ def kv_write(kv: KvDesc, k, v, x_dtype: int, slots, cache, tokens: int | None = 
              v_stride: int | None = None, stream=None):
     """Keys and values of new tokens into their slots (bitq_kv_write).  k, v: tensors [tokens, kv_heads,
     head_dim] whose last two dimensions are contiguous (or addresses, with the strides given)."""
-    _check(_lib.bitq_kv_write(kv, _ptr(k), _ptr(v), x_dtype, k.stride(0) if k_stride is None else k_stride,
-                              v.stride(0) if v_stride is None else v_stride, _ptr(slots),
-                              slots.numel() if tokens is None else tokens, _ptr(cache), _nbytes(cache), _stream(stream)))
+    _check(_lib.bitq_kv_write(kv, _addr(k), _addr(v), x_dtype, k.stride(0) if k_stride is None else k_stride,
+                              v.stride(0) if v_stride is None else v_stride, _addr(slots),
+                              slots.numel() if tokens is None else tokens, _addr(cache), _nbytes(cache), _stream(stream)))
 
 
 def attn_desc(kv: KvDesc, heads: int, requests: int, table_stride: int, max_len: int, window: int = 0,
@@ -490,8 +505,8 @@ def paged_attn_workspace(desc: AttnDesc) -> int:
 def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_stride: int | None = None,
                ws_bytes: int | None = None, stream=None):
     """Attention of one new token per request over the paged cache (bitq_paged_attn)."""
-    _check(_lib.bitq_paged_attn(desc, _ptr(q), q.stride(0) if q_stride is None else q_stride, _ptr(cache),
-                                _nbytes(cache), _ptr(table), _ptr(lens), _ptr(out), _ptr(lse), _ptr(ws),
+    _check(_lib.bitq_paged_attn(desc, _addr(q), q.stride(0) if q_stride is None else q_stride, _addr(cache),
+                                _nbytes(cache), _addr(table), _addr(lens), _addr(out), _addr(lse), _addr(ws),
                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
@@ -506,8 +521,8 @@ def norm_desc(rows: int, width: int, u_dtype: int = DT_F32, r_dtype: int = DT_F3
 
 def block_norm(desc: NormDesc, u, r, post, gate, pre, r_out, h, d=None, stream=None):
     """Residual update with the norms before and after it (bitq_block_norm); d: the rows' scales (DT_ROW8)."""
-    _check(_lib.bitq_block_norm(desc, _ptr(u), _ptr(r), _ptr(post), _ptr(gate), _ptr(pre), _ptr(r_out), _ptr(h),
-                                _ptr(d), _stream(stream)))
+    _check(_lib.bitq_block_norm(desc, _addr(u), _addr(r), _addr(post), _addr(gate), _addr(pre), _addr(r_out), _addr(h),
+                                _addr(d), _stream(stream)))
 
 
 def w8a8_desc(M: int, N: int, K: int, y_dtype: int = DT_F32, lda: int | None = None, ldw: int | None = None,
@@ -522,7 +537,7 @@ def w8a8_workspace(desc: W8A8Desc) -> int:
 
 def gemm_w8a8(desc: W8A8Desc, a, a_scale, w, w_scale, y, ws=None, ws_bytes: int | None = None, stream=None):
     """y = diag(a_scale) a w^T diag(w_scale) on int8 rows (bitq_gemm_w8a8)."""
-    _check(_lib.bitq_gemm_w8a8(desc, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(y), _ptr(ws),
+    _check(_lib.bitq_gemm_w8a8(desc, _addr(a), _addr(a_scale), _addr(w), _addr(w_scale), _addr(y), _addr(ws),
                                _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
