@@ -74,11 +74,16 @@ __device__ __forceinline__ void put(const GemmArgs& g, int64_t m, int n, int acc
 // round-robin, and add their sums in LDS at the end.  A wave has a ring of NS
 // units of its own in LDS, so the waves never wait for each other: the wave
 // keeps NS - 1 units of copies in flight and waits for the oldest one only.
-template <int TT, int NB, int KW, int NS>
+//
+// TC = 1: at most 8 tokens, one copy brings them (rows 8 .. 15 of the tile
+// then hold another unit's bytes; their products are not stored).
+template <int TT, int NB, int KW, int NS, int TC = 2 * TT>
 __global__ __launch_bounds__(64 * KW) void w8a8_few_kernel(GemmArgs g) {
-    constexpr int ROWB = 128, PER = 2 * (TT + NB), UNIT = PER * 1024;  // copies and bytes of a unit (2 copies a tile)
+    static_assert(TC == 2 * TT || (TT == 1 && TC == 1), "two copies a tile, or one of 8 tokens");
+    constexpr int ROWB = 128, PER = 2 * NB + TC, UNIT = PER * 1024;  // copies and bytes of a unit (2 copies a tile)
     constexpr int SUMS = KW * TT * NB * 4 * 68 * 4;
-    __shared__ __align__(1024) uint8_t s_mem[KW * NS * UNIT > SUMS ? KW * NS * UNIT : SUMS];
+    constexpr int RINGS = KW * NS * UNIT + (TC == 1 ? 1024 : 0);  // (TC = 1: the last unit's missing rows lie past it)
+    __shared__ __align__(1024) uint8_t s_mem[RINGS > SUMS ? RINGS : SUMS];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int grp = lane >> 4, r = lane & 15;
     const int n0 = 16 * NB * blockIdx.x;
@@ -371,9 +376,20 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(GemmArgs g, int tiles_m,
 }
 
 // Which kernel takes a call.  Measured on MI355X, weights from HBM, us:
-//   up to 16 tokens, channel tiles per workgroup 1 / 2 / 4: N = 1024 3.5 / 4.0
-//     / 5.1, 4096 6.0 / 5.6 / 6.2, 6000 8.9 / 6.6 / 7.2, 11008 13.7 / 12.2 /
-//     10.2 (K = 4096; 4.4 TB/s of weights)
+//   1 token; one channel tile a workgroup and 16 waves with rings of 3 / four
+//     tiles, 8 waves, rings of 2 / one tile, 4 waves, rings of 5:
+//       N = 2000, K = 4096    3.4 /  4.9 /  3.1
+//       4096, 4096            4.6 /  6.0 /  5.0   (3.7 TB/s of weights)
+//       4096, 11008           8.9 / 13.2 /  8.9   (5.1)
+//       6000, 4096            7.5 /  7.4 /  7.1
+//       11008, 4096          11.2 /  9.6 / 11.9   (4.7)
+//       28672, 8192          44.6 / 47.3 / 40.7   (5.8)
+//     so the first while every workgroup has a CU of its own (N <= 4096), the
+//     second while four tiles do that (N <= 16384), the third beyond.
+//   16 tokens: a ring of 16 waves does not fit with their 2 KiB of tokens a
+//     unit; one tile and 8 waves with rings of 4 instead, 5.6 / 6.5 / 6.3 at
+//     4096 x 4096, and 13.6 / 9.7 / 13.0 at 11008 x 4096, 54.2 / 48.1 / 46.5
+//     at 28672 x 8192.
 //   24 tokens: few-token kernel 16.4 against 64 x 64 tiles 11.6 at N = 11008,
 //     12.1 against 13.7 (4 k ranges) at N = 4096, K = 11008
 //   40 tokens: 19.2 against 11.8; 14.7 against 14.2
@@ -417,9 +433,9 @@ W8A8Plan w8a8_plan(const bitq_w8a8_desc& d) {
     return p;
 }
 
-template <int TT, int NB, int KW, int NS>
+template <int TT, int NB, int KW, int NS, int TC = 2 * TT>
 static int launch_few(const GemmArgs& g, hipStream_t st) {
-    hipLaunchKernelGGL((w8a8_few_kernel<TT, NB, KW, NS>), dim3(static_cast<unsigned>((g.N + 16 * NB - 1) / (16 * NB))),
+    hipLaunchKernelGGL((w8a8_few_kernel<TT, NB, KW, NS, TC>), dim3(static_cast<unsigned>((g.N + 16 * NB - 1) / (16 * NB))),
                        dim3(64 * KW), 0, st, g);
     return static_cast<int>(hipGetLastError());
 }
@@ -449,9 +465,9 @@ int launch_gemm_w8a8(const bitq_w8a8_desc& d, const W8A8Plan& plan, const void* 
     hipStream_t st = static_cast<hipStream_t>(stream);
     switch (plan.kernel) {
         case 1:
-            if (d.N <= 2048) return launch_few<1, 1, 8, 4>(g, st);
-            if (d.N <= 8192) return launch_few<1, 2, 8, 3>(g, st);
-            return launch_few<1, 4, 8, 2>(g, st);
+            if (d.N <= 4096) return d.M <= 8 ? launch_few<1, 1, 16, 3, 1>(g, st) : launch_few<1, 1, 8, 4>(g, st);
+            if (d.N <= 16384) return launch_few<1, 4, 8, 2>(g, st);
+            return launch_few<1, 1, 4, 5>(g, st);
         case 2: return launch_few<2, 1, 8, 3>(g, st);
         case 3: return launch_few<3, 1, 8, 2>(g, st);
         case 4: return launch_few<4, 1, 8, 2>(g, st);
