@@ -51,12 +51,14 @@ struct AttnArgs {
     int R, H, A, group, tiles, D, page_shift, pages, table_stride, max_len, window;
     float c;           // scale log2(e): p = 2^(c s - m)
     int qdt, odt;
+    int qvec;          // 16-byte loads of q: D a multiple of 8, rows and base aligned
 };
 
 // Tokens [lo, hi) of request r.
+__device__ __forceinline__ int first_token(const AttnArgs& a, int hi) { return a.window > 0 ? max(hi - a.window, 0) : 0; }
 __device__ __forceinline__ void token_range(const AttnArgs& a, int r, int& lo, int& hi) {
     hi = min(max(a.lens[r], 0), a.max_len);
-    lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+    lo = first_token(a, hi);
 }
 // Passes of a workgroup over [lo, hi): steps are aligned to 32 tokens.
 __device__ __forceinline__ int token_units(int lo, int hi) {
@@ -136,7 +138,7 @@ struct AttnWave {
     const int lane, g, j;
     const __bf16* sq;    // the query tile's operands in LDS: [NQ][NC][64 lanes][8]
     const int32_t* row;  // the request's row of the table
-    int h, lo, hi;
+    int h, lo, hi, last;
 
     __device__ __forceinline__ AttnWave(const AttnArgs& args, int ln, const __bf16* s)
         : a(args), lane(ln), g(ln >> 4), j(ln & 15), sq(s) {}
@@ -145,11 +147,14 @@ struct AttnWave {
         return *reinterpret_cast<const bf16x8_t*>(sq + ((n * NC + c) * 64 + lane) * 8);
     }
 
-    __device__ __forceinline__ void begin(int r, int hk, int lo_, int hi_) {
+    __device__ __forceinline__ void range(int r, int hk, int lo_, int hi_) {
         h = hk;
         lo = lo_;
         hi = hi_;
+        last = max(hi - 1, 0);  // (an empty request reads what its table's first place names, and uses none of it)
         row = a.table + static_cast<size_t>(r) * a.table_stride;
+    }
+    __device__ __forceinline__ void begin() {
         if constexpr (!HI) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) q[c] = q_operand(0, c);
@@ -165,9 +170,9 @@ struct AttnWave {
     // tiles, V group (and scales).
     __device__ __forceinline__ void tokens(int s, int (&tok)[3]) const {
         const int k = s + 8 * (j >> 2) + (j & 3);
-        tok[0] = min(max(k, lo), hi - 1);
-        tok[1] = min(max(k + 4, lo), hi - 1);
-        tok[2] = min(max(s + 8 * g, lo & ~7), (hi - 1) & ~7);
+        tok[0] = min(max(k, lo), last);
+        tok[1] = min(max(k + 4, lo), last);
+        tok[2] = min(max(s + 8 * g, lo & ~7), last & ~7);
     }
     __device__ __forceinline__ void lookup(int s, int (&pg)[3]) const {
         int tok[3];
@@ -329,36 +334,35 @@ struct AttnWave {
     // The wave's steps s0, s0 + stride, ... below s1.  A step's registers are
     // loaded again as soon as they are free: the next keys are in flight
     // while the weights and values are worked on, the next values while the
-    // next scores are.  (The loads are unconditional, the last step's are
-    // repeated: behind a branch the compiler would wait for all of them.  A
-    // second set of registers, or the first loads issued before the queries
-    // are staged, measured no better.)
+    // next scores are.  The last step, which loads nothing, is code of its
+    // own: behind a branch in the loop the compiler would wait for all loads.
+    // (A second set of registers measured no better.)
+    template <bool LAST>
     __device__ __forceinline__ void step(int s, int next, int after, AttnStep<KVT, NC>& L, int (&pg)[3]) {
         const bool edge = s < lo || s + 32 > hi;  // (the same for the whole wave)
         float x[8];
         uint32_t keep;
         asm volatile("" ::: "memory");  // (q's operands are read again, not kept in registers)
         scores(s, L, x, keep, edge);
-        load_k(next, pg, L);
+        if constexpr (!LAST) load_k(next, pg, L);
         weights(x);
         values(L, x, keep, edge);
-        load_v(next, pg, L);
-        lookup(after, pg);
+        if constexpr (!LAST) {
+            load_v(next, pg, L);
+            lookup(after, pg);
+        }
     }
-    __device__ __forceinline__ void run(int s0, int s1, int stride) {
-        if (s0 >= s1) return;
-        AttnStep<KVT, NC> L;
-        int pg[3];
-        auto upto = [&](int s) { return s < s1 ? s : s0; };
+    __device__ __forceinline__ void first(int s0, int s1, int stride, AttnStep<KVT, NC>& L, int (&pg)[3]) {
         lookup(s0, pg);
         load_k(s0, pg, L);
         load_v(s0, pg, L);
-        lookup(upto(s0 + stride), pg);
-        for (int s = s0;;) {
-            step(s, upto(s + stride), upto(s + 2 * stride), L, pg);
-            s += stride;
-            if (s >= s1) return;
-        }
+        if (s0 + stride < s1) lookup(s0 + stride, pg);
+    }
+    __device__ __forceinline__ void run(int s0, int s1, int stride, AttnStep<KVT, NC>& L, int (&pg)[3]) {
+        if (s0 >= s1) return;
+        int s = s0;
+        for (; s + stride < s1; s += stride) step<false>(s, s + stride, min(s + 2 * stride, last), L, pg);
+        step<true>(s, 0, 0, L, pg);
     }
 
     // O, m, l to the wave's part of LDS: so [16][Dp + 4], sm and sl [16].
@@ -392,6 +396,41 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
+// Sum over lanes 0 .. this lane.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // from 1, 2, 4 and 8 lanes below, in a row of 16
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of a row to the row above: rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
+    return v;
+}
+
+// The deal of T units to G workgroups (at most 1024): workgroup i has units
+// [start(i), start(i + 1)), start(i) = floor(T i / G).  With T = q G + rem it is
+// i q + floor(rem i / G), and rem i < 2^20, so the fp32 quotient of rem i +
+// 1/2 is off by less than 1/(2 G) and rounds down to the right integer.
+struct AttnRanges {
+    uint32_t T, G, q, rem;
+    float inv;
+    __device__ __forceinline__ AttnRanges(uint32_t units, uint32_t grid) : T(units), G(min(units, grid)) {
+        q = T / max(G, 1u);
+        rem = T - q * G;
+        inv = 1.0f / static_cast<float>(G);
+    }
+    __device__ __forceinline__ uint32_t start(uint32_t i) const {
+        return i * q + static_cast<uint32_t>((static_cast<float>(rem * i) + 0.5f) * inv);
+    }
+    // the workgroup that has unit x < T
+    __device__ __forceinline__ uint32_t owner(uint32_t x) const {
+        uint32_t i = min(static_cast<uint32_t>(static_cast<float>(x) / static_cast<float>(T) * static_cast<float>(G)), G - 1);
+        while (start(i) > x) --i;
+        while (start(i + 1) <= x) ++i;
+        return i;
+    }
+};
+
 // First index i in [0, n) with a[i] > x (n if none); a ascending.
 __device__ __forceinline__ int first_above32(const int32_t* a, int n, int x) {
     int lo = 0, hi = n;
@@ -416,7 +455,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) v
     constexpr int Dp = 32 * NC, W = kAttnWaves, ROW = Dp + 4;
     __shared__ __align__(16) float s_o[W][16 * ROW];
     __shared__ float s_m[W][16], s_l[W][16];
-    constexpr int NQ = HI ? 3 : 1;
+    constexpr int NQ = HI ? 3 : 1, QP = (2 * Dp + 64 * W - 1) / (64 * W);
     __shared__ __align__(16) __bf16 s_q[NQ * 16 * Dp];
     extern __shared__ int32_t s_pre[];  // SPLIT: [R + 1]
     __shared__ int32_t s_scan[W];
@@ -426,58 +465,76 @@ __global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) v
 
     int x = blockIdx.x, x1 = x + 1;  // units (SPLIT; fewer than 2^31) or the item
     int U = 1;
+    // up to 64 requests: lane r of every wave keeps request r's length and
+    // the end of its units, and a unit's request is found by one vote; more:
+    // the prefix sums are in LDS and searched (lens read again)
+    const bool few = a.R <= 64;
+    int my_hi = 0, my_end = 0;
     if constexpr (SPLIT) {
-        int carry = 0;
-        for (int r0 = 0; r0 < a.R; r0 += 64 * W) {
-            const int r = r0 + tid;
-            int u = 0;
-            if (r < a.R) {
-                int lo, hi;
-                token_range(a, r, lo, hi);
-                u = token_units(lo, hi);
+        if (few) {
+            int lo = 0;
+            if (lane < a.R) token_range(a, lane, lo, my_hi);
+            my_end = wave_scan(token_units(lo, my_hi));
+            U = __builtin_amdgcn_readlane(my_end, 63);
+            if (blockIdx.x == 0 && wave == 0) {
+                if (lane < a.R) a.prefix[lane + 1] = my_end;
+                if (lane == 0) a.prefix[0] = 0;
             }
-            int inc = u;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int t = __shfl_up(inc, o, 64);
-                if (lane >= o) inc += t;
+        } else {
+            int carry = 0;
+            for (int r0 = 0; r0 < a.R; r0 += 64 * W) {
+                const int r = r0 + tid;
+                int lo = 0, hi = 0;
+                if (r < a.R) token_range(a, r, lo, hi);
+                int inc = wave_scan(token_units(lo, hi));
+                __syncthreads();
+                if (lane == 63) s_scan[wave] = inc;
+                __syncthreads();
+                int all = 0;
+                for (int i = 0; i < W; ++i) {
+                    if (i < wave) inc += s_scan[i];
+                    all += s_scan[i];
+                }
+                if (r < a.R) s_pre[r + 1] = carry + inc;
+                carry += all;
             }
+            if (tid == 0) s_pre[0] = 0;
             __syncthreads();
-            if (lane == 63) s_scan[wave] = inc;
-            __syncthreads();
-            int all = 0;
-            for (int i = 0; i < W; ++i) {
-                if (i < wave) inc += s_scan[i];
-                all += s_scan[i];
-            }
-            if (r < a.R) s_pre[r + 1] = carry + inc;
-            carry += all;
+            if (blockIdx.x == 0)
+                for (int r = tid; r <= a.R; r += 64 * W) a.prefix[r] = s_pre[r];
+            U = wave_uniform(s_pre[a.R]);
         }
-        if (tid == 0) s_pre[0] = 0;
-        __syncthreads();
-        if (blockIdx.x == 0)
-            for (int r = tid; r <= a.R; r += 64 * W) a.prefix[r] = s_pre[r];
-        U = wave_uniform(s_pre[a.R]);
-        const int64_t T = static_cast<int64_t>(U) * HT;
+        const uint32_t T = static_cast<uint32_t>(U) * HT;  // (< 2^31)
         // (with fewer units than workgroups the surplus workgroups have none:
         // every range below G is non-empty, which the join relies on)
-        const int64_t G = min(T, static_cast<int64_t>(gridDim.x));
-        if (blockIdx.x >= G) return;
-        x = static_cast<int>(T * blockIdx.x / G);
-        x1 = static_cast<int>(T * (static_cast<int64_t>(blockIdx.x) + 1) / G);
+        const AttnRanges ranges(T, gridDim.x);
+        if (blockIdx.x >= ranges.G) return;
+        x = ranges.start(blockIdx.x);
+        x1 = ranges.start(blockIdx.x + 1);
     }
     while (x < x1) {
         int ht, r, lo, hi, s0, s1;
         bool whole = true;
         int slot = 0, next = x + 1;
         if constexpr (SPLIT) {
-            ht = x / U;
+            ht = static_cast<uint32_t>(x) / static_cast<uint32_t>(U);
             const int rem = x - ht * U;
-            r = wave_uniform(first_above32(s_pre + 1, a.R, rem));
-            token_range(a, r, lo, hi);
-            const int end = ht * U + wave_uniform(s_pre[r + 1]);
+            int begin, end;  // of the request's units
+            if (few) {
+                r = __builtin_ctzll(__ballot(my_end > rem));  // (rem < U = the last lane's)
+                hi = __builtin_amdgcn_readlane(my_hi, r);
+                lo = first_token(a, hi);
+                end = __builtin_amdgcn_readlane(my_end, r);
+                begin = r > 0 ? __builtin_amdgcn_readlane(my_end, r - 1) : 0;
+            } else {
+                r = wave_uniform(first_above32(s_pre + 1, a.R, rem));
+                token_range(a, r, lo, hi);
+                begin = wave_uniform(s_pre[r]);
+                end = wave_uniform(s_pre[r + 1]);
+            }
+            end += ht * U;
             next = min(x1, end);
-            const int k0 = rem - wave_uniform(s_pre[r]);
+            const int k0 = rem - begin;
             whole = k0 == 0 && next == end;
             slot = k0 == 0 ? 1 : 0;
             s0 = (lo & ~31) + k0 * kAttnUnit;
@@ -490,24 +547,59 @@ __global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) v
             s1 = hi;
         }
         // (values that are the same for the whole wave, kept in scalar registers)
-        const int hk = ht / a.tiles, tile = ht - hk * a.tiles, heads = min(16, a.group - 16 * tile);
-        // ---- the tile's queries into LDS, as the terms and in the order of the operands
+        const int hk = static_cast<uint32_t>(ht) / static_cast<uint32_t>(a.tiles), tile = ht - hk * a.tiles;
+        const int heads = min(16, a.group - 16 * tile);
+        // ---- the tile's queries, 8 elements of a head at a time; then the first step's loads, behind them
         const int64_t qat = static_cast<int64_t>(r) * a.q_stride + (static_cast<int64_t>(hk) * a.group + 16 * tile) * a.D;
-        for (int i = tid; i < 16 * Dp; i += 64 * W) {
-            const int head = i / Dp, d = i - head * Dp;
-            float v = 0.0f;
-            if (head < heads && d < a.D) v = load_act(a.q, a.qdt, static_cast<size_t>(qat + head * a.D + d));
-            const int at = q_place<KVT == BITQ_KV_INT8, NC>(d, head);
+        const bool q32 = HI && a.qdt == BITQ_DT_F32;
+        uint32_t qv[QP][8];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const __bf16 b = static_cast<__bf16>(v);
-                s_q[n * (16 * Dp) + at] = b;
-                v -= static_cast<float>(b);
+        for (int u = 0; u < QP; ++u) {
+            const int i = tid + 64 * W * u, head = min(i / (Dp / 8), heads - 1), d = 8 * (i % (Dp / 8));
+            // (as loaded: a conversion here would wait for the loads)
+            if (a.qvec) {
+                const uint8_t* p = static_cast<const uint8_t*>(a.q) + (qat + head * a.D + min(d, a.D - 8)) * (q32 ? 4 : 2);
+                const uint4 v0 = reinterpret_cast<const uint4*>(p)[0];
+                qv[u][0] = v0.x, qv[u][1] = v0.y, qv[u][2] = v0.z, qv[u][3] = v0.w;
+                if (q32) {
+                    const uint4 v1 = reinterpret_cast<const uint4*>(p)[1];
+                    qv[u][4] = v1.x, qv[u][5] = v1.y, qv[u][6] = v1.z, qv[u][7] = v1.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t at = head * a.D + min(d + e, a.D - 1);
+                    if (q32) qv[u][e] = (static_cast<const uint32_t*>(a.q) + qat)[at];
+                    else qv[u][e] = (static_cast<const uint16_t*>(a.q) + qat)[at];
+                }
             }
         }
+        AttnStep<KVT, NC> L;
+        int pg[3];
+        const int from = wave_uniform(s0) + 32 * wave, upto = wave_uniform(s1);
+        w.range(r, hk, wave_uniform(lo), wave_uniform(hi));
+        w.first(from, upto, kAttnUnit, L, pg);
+        // ---- into LDS as the terms and in the order of the operands
+#pragma unroll
+        for (int u = 0; u < QP; ++u) {
+            const int i = tid + 64 * W * u, head = i / (Dp / 8), d = 8 * (i % (Dp / 8));
+            if (i >= 2 * Dp) break;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t pair = qv[u][e / 2];
+                const uint32_t bits = q32 ? qv[u][e] : !a.qvec ? qv[u][e] << 16 : e & 1 ? pair & 0xFFFF0000u : pair << 16;
+                f[e] = head < heads && d + e < a.D ? __uint_as_float(bits) : 0.0f;
+            }
+            bf16x8_t t[NQ];
+            split_terms<NQ>(f, t);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+                *reinterpret_cast<bf16x8_t*>(s_q + n * (16 * Dp) + q_place<KVT == BITQ_KV_INT8, NC>(d, head)) = t[n];
+        }
         __syncthreads();
-        w.begin(r, hk, wave_uniform(lo), wave_uniform(hi));
-        w.run(wave_uniform(s0) + 32 * wave, wave_uniform(s1), kAttnUnit);
+        w.begin();
+        w.run(from, upto, kAttnUnit, L, pg);
         w.park(s_o[wave], s_m[wave], s_l[wave]);
         __syncthreads();
         float* part = SPLIT ? a.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (16 * (Dp + 2)) : nullptr;
@@ -549,19 +641,18 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void attn_join_kernel(Attn
     constexpr int HPB = NW == 1 ? 4 : 1;
     __shared__ float s_acc[NW][256], s_m[NW], s_l[NW];
     const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
-    const int64_t qa = static_cast<int64_t>(blockIdx.x) * HPB + (NW == 1 ? wave : 0);
-    if (qa >= static_cast<int64_t>(a.R) * a.A) return;
-    const int r = static_cast<int>(qa / a.A), qh = static_cast<int>(qa - static_cast<int64_t>(r) * a.A);
-    const int hk = qh / a.group, in = qh - hk * a.group, ht = hk * a.tiles + (in >> 4), head = in & 15;
-    const int64_t U = a.prefix[a.R], u0 = a.prefix[r], u1 = a.prefix[r + 1];
+    // (requests x heads is below 2^31: requests is at most 4096 here, heads 32-bit checked below)
+    const uint32_t qa = blockIdx.x * HPB + (NW == 1 ? wave : 0);
+    if (qa >= static_cast<uint32_t>(a.R) * a.A) return;
+    const int r = qa / static_cast<uint32_t>(a.A), qh = qa - r * a.A;
+    const int hk = static_cast<uint32_t>(qh) / static_cast<uint32_t>(a.group), in = qh - hk * a.group, ht = hk * a.tiles + (in >> 4), head = in & 15;
+    const int U = a.prefix[a.R], u0 = a.prefix[r], u1 = a.prefix[r + 1];
     float acc[4] = {0, 0, 0, 0}, M = -FLT_MAX, L = 0.0f;
     if (u1 > u0) {
-        const int64_t T = U * a.H * a.tiles, b = ht * U, G = min(T, static_cast<int64_t>(main_grid));
-        // the workgroup whose range [T i / G, T (i + 1) / G) holds unit x is
-        // the largest i with T i / G < x + 1
-        const int64_t i0 = ((b + u0 + 1) * G - 1) / T, i1 = ((b + u1) * G - 1) / T;
+        const AttnRanges ranges(U * a.H * a.tiles, main_grid);
+        const int i0 = ranges.owner(ht * U + u0), i1 = ranges.owner(ht * U + u1 - 1);
         if (i0 == i1) return;  // whole in one range: written there
-        for (int64_t i = i0 + (NW == 1 ? 0 : wave); i <= i1; i += NW) {
+        for (int i = i0 + (NW == 1 ? 0 : wave); i <= i1; i += NW) {
             const float* p = a.part + (static_cast<size_t>(i) * 2 + (i == i0 ? 1 : 0)) * (16 * (Dp + 2));
             const float pm = p[16 * Dp + head], pl = p[16 * Dp + 16 + head];
             float v[4];
@@ -663,6 +754,8 @@ int launch_paged_attn(const bitq_attn_desc& d, const AttnPlan& plan, const void*
     a.c = d.scale * 1.44269504088896340736f;
     a.qdt = d.q_dtype;
     a.odt = d.out_dtype;
+    const int per16 = d.q_dtype == BITQ_DT_F32 ? 4 : 8;
+    a.qvec = a.D % 8 == 0 && q_stride % per16 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
     if (d.kv.dtype == BITQ_KV_BF16) {

@@ -297,6 +297,9 @@ ATTN = [
     (70, 8, 2, 64, 16, "ragged", False, False, False, 0),
     (70, 8, 2, 64, 16, "ragged", True, True, True, 77),
     (600, 1, 1, 33, 8, "short", False, False, True, 0),             # requests beyond one scan round
+    (64, 2, 4, 128, 16, "ragged", False, False, False, 0),          # lengths in one wave's registers: the most, and one more
+    (65, 2, 4, 128, 16, "ragged", False, False, False, 0),
+    (64, 1, 4, 88, 16, "ragged", True, True, False, 300),
 ]
 
 
@@ -349,6 +352,17 @@ def test_attention_ignores_what_is_outside(int8, window):
     dirty = run_attention(K, V, ks, vs, q, table, lens, page, 0.125, window, 300, False, True, poison=poison)
     assert np.array_equal(clean[0], dirty[0]) and np.array_equal(clean[1], dirty[1])
     assert np.all(clean[0][2] == 0) and np.all(clean[1][2] == -np.inf)
+
+
+@pytest.mark.parametrize("qf32", [False, True])
+def test_attention_takes_any_row_stride_of_q(qf32):
+    """Rows of q that 16-byte loads can take, and rows that they cannot: the same result."""
+    say("attn q stride", qf32)
+    rng = np.random.default_rng(16)
+    K, V, ks, vs, q, table = attention_case(rng, 3, 2, 5, 64, 16, [200, 33, 64], False, qf32)
+    runs = [run_attention(K, V, ks, vs, q, table, [200, 33, 64], 16, 0.125, 0, 200, qf32, True, q_pad=p) for p in (0, 8, 4, 3, 1)]
+    for o, l in runs[1:]:
+        assert np.array_equal(o, runs[0][0]) and np.array_equal(l, runs[0][1])
 
 
 def test_attention_lengths_and_pages_outside_their_range():
