@@ -300,6 +300,9 @@ ATTN = [
     (64, 2, 4, 128, 16, "ragged", False, False, False, 0),          # lengths in one wave's registers: the most, and one more
     (65, 2, 4, 128, 16, "ragged", False, False, False, 0),
     (64, 1, 4, 88, 16, "ragged", True, True, False, 300),
+    (1, 1, 3, 64, 64, [70000], False, True, True, 0),               # hundreds of partial results for each head
+    (17, 1, 1, 64, 32, [100000] + [1] * 16, True, True, True, 0),
+    (600, 1, 1, 40, 16, [20000, 0, 3] * 2 + [1] * 594, False, False, True, 0),
 ]
 
 
