@@ -513,8 +513,11 @@ static void launch_write(const WriteArgs& a, hipStream_t st) {
         ++shift;
     }
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.heads;
-    // 8 tokens per thread once single tokens would give more than 2^16 threads
-    if (rows * LR <= (1 << 16)) {
+    // 8 tokens per thread once single tokens would give more than 2^17
+    // threads.  Measured, bf16, runs of 100 slots (single slots), us with 1 / 8
+    // tokens: 2^16 threads 5.3 / 10.3 (7.2 / 14.9), 2^17 8.9 / 9.5 (10.6 /
+    // 17.6), 2^18 15.4 / 10.7 (17.3 / 21.9), 2^20 50.5 / 21.4 (78 / 81).
+    if (rows * LR <= (1 << 17)) {
         const dim3 grid(static_cast<unsigned>((rows * LR + 255) / 256), 2);
         hipLaunchKernelGGL((kv_write_kernel<XDT, KVT, 1>), grid, dim3(256), 0, st, a, LR, shift);
     } else {

@@ -282,12 +282,15 @@ int launch_block_norm(const bitq_norm_desc& d, const void* u, const void* r, con
             ok(h, d.out_dtype, d.h_stride);
     const int chunks = (d.width + 7) / 8;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // many rows: the fewest waves that hold a row; few rows: one chunk a
-    // lane, for the shortest chain
-    const bool many = d.rows >= 1024;
+    // few rows: one chunk a lane, for the shortest chain; many: fewer waves
+    // with more of a row, for more rows at a time on a CU.  Measured, bf16, us:
+    //   width 1024, <1,2> and <4,1>: 1024 rows 4.9 / 4.7, 2048 5.7 / 7.1
+    //   2048, <1,4> (not kept) and <4,1>: 1024 rows 7.2 / 5.6, 4096 13.8 / 14.1
+    //   4096, <4,2> and <16,1>: 256 rows 5.1 / 4.8, 512 6.0 / 8.0
+    //   8192, <4,4> and <16,1>: 256 rows 7.6 / 6.0, 512 10.8 / 10.6, 1024 14.3 / 18.3
+    const bool many = d.rows > 256;
     if (chunks <= 64) launch_norm<1, 1>(a, st);
-    else if (many && chunks <= 128) launch_norm<1, 2>(a, st);
-    else if (many && chunks <= 256) launch_norm<1, 4>(a, st);
+    else if (d.rows > 1024 && chunks <= 128) launch_norm<1, 2>(a, st);
     else if (chunks <= 256) launch_norm<4, 1>(a, st);
     else if (many && chunks <= 512) launch_norm<4, 2>(a, st);
     else if (many && chunks <= 1024) launch_norm<4, 4>(a, st);

@@ -163,6 +163,12 @@ def test_plan_steps_in_turn():
     (1000, 3, 255, 1024, True, True, "runs"),
     (2500, 2, 72, 16, True, False, "mixed"),
     (5000, 1, 40, 8, False, False, "mixed"),
+    (1200, 8, 128, 64, False, False, "runs"),                        # from here on 8 tokens a thread
+    (1400, 8, 128, 64, True, False, "runs"),
+    (2000, 3, 255, 1024, True, True, "runs"),
+    (16000, 2, 72, 16, True, False, "mixed"),
+    (16000, 2, 72, 8, False, False, "mixed"),
+    (30000, 1, 80, 8, False, True, "mixed"),
 ])
 def test_write(T, H, D, page, int8, f32, mode):
     import torch
@@ -441,7 +447,8 @@ def host(t, dt):
 
 
 @pytest.mark.parametrize("M,C", [(1, 1), (1, 4096), (3, 7), (5, 64), (2, 513), (4, 1000), (1, 11008), (3, 28672), (2, 32768),
-                                 (2, 32767), (1300, 96), (1100, 2048), (1030, 4104), (70, 8192)])
+                                 (2, 32767), (1300, 96), (1100, 2048), (1030, 4104), (70, 8192),
+                                 (1100, 1000), (300, 4000)])
 @pytest.mark.parametrize("udt,rdt,wdt,odt,post,gate,resid", [
     ("f", "f", "f", "f", True, "channel", True),
     ("b", "b", "b", "b", True, "token", True),
