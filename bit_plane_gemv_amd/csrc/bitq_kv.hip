@@ -27,7 +27,9 @@ namespace bitq {
 // associative, so a scan of it is exact up to there, and every limit that a
 // sum is compared with is below 2^29).
 //
-// Bound by latency: two dependent loads, the scan and one search.
+// Bound by latency: two dependent loads, the scan and one search.  64
+// requests of one new token each 4.0 us, 1024 requests with 65536 new tokens
+// (0.8 MB written) 7.2 us.
 struct PlanOut {
     int32_t *state, *len, *start, *slot, *req, *pos;
 };
@@ -245,7 +247,7 @@ int launch_kv_plan(const bitq_kv_plan_desc& d, const int32_t* old_len, const int
 // 8 consecutive slots: it reads 8 rows' 16 bytes and transposes in registers.
 // Its 8 pieces of 16 bytes are 128 bytes apart from the next lane's; they are
 // exchanged through LDS inside the wave, so that every store instruction
-// writes 1 KB in a row (prompts of 4096 tokens, 32 heads of 128: 53 -> 37 us).
+// writes 1 KB in a row (prompts of 4096 tokens, 32 heads of 128: 53 -> 38 us).
 // TG = 8: a thread owns the groups that begin among its 8 tokens of the list
 // (groups of consecutive slots are found from the slots, whatever their
 // alignment to the list; at most one of them is whole); a group that is not
@@ -256,7 +258,11 @@ int launch_kv_plan(const bitq_kv_plan_desc& d, const int32_t* old_len, const int
 // activation quantizer.
 //
 // Bound by HBM for long prompts (each element read and written once), by
-// latency for decode.
+// latency for decode.  Prompts of 4096 tokens, 32 heads of 128, bf16: 38 us,
+// 134 MB at 3.5 TB/s (a copy of those bytes takes 26 us; K alone 14, at the
+// copy's rate, V 22: its loads have to wait for the slots).  64 tokens of 8
+// heads: 3.8 us.
+//
 // 8 elements of a row as loaded (converted where they are used: 8 rows of
 // bf16 then take 32 registers).
 template <int XDT>

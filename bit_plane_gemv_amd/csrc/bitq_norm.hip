@@ -17,7 +17,9 @@ namespace bitq {
 // Sums, r' and h are fp32; r' is rounded only where it is stored, and h is
 // taken from the unrounded r'.  One wave per row needs no barrier (4 rows
 // per workgroup); more waves meet in LDS.  Bound by HBM for many rows, by
-// the latency of one round of loads and the reductions for few.
+// the latency of one round of loads and the reductions for few: 4096 rows of
+// 8192 with a gate per token, bf16, 71 us (336 MB, 4.7 TB/s, the rate of a
+// copy); one row of 4096, fp32, 3.7 us.
 struct NormArgs {
     const void *u, *r, *post, *gate, *pre;
     void *ro, *h;
@@ -26,24 +28,30 @@ struct NormArgs {
     float res, branch, eps_post, eps_pre;
     int M, C;
     int udt, rdt, wdt, odt;
-    bool vec;  // every row chunk of 8 is 16-byte aligned, and C a multiple of 8
+    bool vec;  // every row chunk of 8 is 16-byte aligned
 };
+
+constexpr int kAnyType = -1;  // of rows that 16-byte loads cannot take: one kernel, types at run time
 
 // 8 elements of a row as loaded (4 registers in bf16, 8 in fp32), converted
 // where they are used: a row then stays in few enough registers for four or
-// more rows per CU.
+// more rows per CU, and no load waits for another.  Elements k .. k + 7 of the
+// row at `at`, the first n of them present (the rest 0).
+//
+// kAnyType: element e of the chunk is k + e T instead, so that the lanes of a
+// load are neighbours (bf16, 1947 rows of 4231: 60 -> 25.5 us).
 template <int DT>
 struct Chunk {
     uint4 a[DT == BITQ_DT_F32 ? 2 : 1];
-    __device__ __forceinline__ float operator[](int e) const {
+    __device__ __forceinline__ float at(int e, int) const {
         const uint4 q = a[DT == BITQ_DT_F32 ? e >> 2 : 0];
         const int w = DT == BITQ_DT_F32 ? e & 3 : e >> 1;
         const uint32_t u = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
         if (DT == BITQ_DT_F32) return __uint_as_float(u);
         return __uint_as_float((e & 1) ? u & 0xFFFF0000u : u << 16);
     }
-    // elements i .. i + 7 of p, the first n of them present (the rest 0)
-    __device__ __forceinline__ void load(const void* p, int64_t i, int n, bool vec) {
+    __device__ __forceinline__ void load(const void* p, int, int64_t at, int k, int n, int, bool vec) {
+        const int64_t i = at + k;
         if (DT == BITQ_DT_F32) {
             const float* f = static_cast<const float*>(p) + i;
             if (vec) {
@@ -72,6 +80,28 @@ struct Chunk {
         a[0] = make_uint4(0, 0, 0, 0);
         a[DT == BITQ_DT_F32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
     }
+};
+// A row of C elements as a buffer of its bytes: elements past its end read as
+// 0 and are not stored, so nothing has to be compared or masked.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t at, int C, int size) {
+    return buffer_rsrc(static_cast<const uint8_t*>(p) + at * size, static_cast<uint32_t>(C * size));
+}
+template <>
+struct Chunk<kAnyType> {
+    uint32_t u[8];
+    __device__ __forceinline__ float at(int e, int dt) const { return __uint_as_float(u[e] << (dt == BITQ_DT_F32 ? 0 : 16)); }
+    __device__ __forceinline__ void load(const void* p, int dt, int64_t at, int k, int C, int step, bool) {
+        if (dt == BITQ_DT_F32) {
+            const auto b = row_buffer(p, at, C, 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = __builtin_amdgcn_raw_buffer_load_b32(b, 4 * (k + e * step), 0, 0);
+        } else {
+            const auto b = row_buffer(p, at, C, 2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = __builtin_amdgcn_raw_buffer_load_b16(b, 2 * (k + e * step), 0, 0);
+        }
+    }
+    __device__ __forceinline__ void zero() {}
 };
 
 __device__ __forceinline__ uint16_t norm_bf16(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
@@ -120,6 +150,23 @@ __device__ __forceinline__ void norm_store(void* p, int dt, int64_t i, int n, bo
     }
 }
 
+__device__ __forceinline__ void norm_store_any(void* p, int dt, int64_t at, int k, int C, int step, const float (&v)[8]) {
+    if (dt == BITQ_DT_F32) {
+        const auto b = row_buffer(p, at, C, 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), b, 4 * (k + e * step), 0, 0);
+    } else if (dt == BITQ_DT_BF16) {
+        const auto b = row_buffer(p, at, C, 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) __builtin_amdgcn_raw_buffer_store_b16(norm_bf16(v[e]), b, 2 * (k + e * step), 0, 0);
+    } else {
+        const auto b = row_buffer(p, at, C, 1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(static_cast<int>(v[e])), b, k + e * step, 0, 0);
+    }
+}
+
 // Sum (or maximum) over the W waves of a row, in a fixed order.
 template <int W, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* s) {
@@ -142,6 +189,10 @@ __device__ __forceinline__ float row_reduce(float v, float* s) {
 template <int W, int NV, int UDT, int RDT, int WDT>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormArgs a) {
     constexpr int T = 64 * W;                // lanes of a row
+    constexpr bool ANY = UDT == kAnyType;    // lanes take neighbouring elements, T apart, instead of 8 in a row
+    auto first = [&](int ln, int j) { return ANY ? 8 * T * j + ln : 8 * (ln + T * j); };
+    // elements present of the chunk at i (<= 0: none); ANY: the row's buffer sees to that
+    auto have = [&](int i) { return ANY ? a.C : min(8, a.C - i); };
     constexpr int RPB = W == 1 ? 4 : 1;      // rows of a workgroup
     // rows of 64 chunks and more per lane-group would not fit the registers
     // with r and the gate held from the start: these are then read late
@@ -150,27 +201,29 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
     // least one barrier, so no wave is more than a row behind
     __shared__ float s_red[2][3][W];
     const int ln = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-    const int sub = W == 1 ? threadIdx.x >> 6 : 0;
+    const int sub = W == 1 ? wave_uniform(threadIdx.x >> 6) : 0;
     int turn = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + sub; row < a.M;
-         row += static_cast<int64_t>(gridDim.x) * RPB, turn ^= 1) {
+    for (int next = blockIdx.x * RPB + sub; next < a.M; next += gridDim.x * RPB, turn ^= 1) {
+        int row_ = wave_uniform(next);
+        if constexpr (ANY) asm volatile("" : "+s"(row_));  // (one address of each buffer in the loop, not one for each element)
+        const int64_t row = row_;
         Chunk<UDT> u[NV];
         Chunk<RDT> r[EARLY ? NV : 1];
         Chunk<WDT> g[EARLY ? NV : 1], po[1], pr[1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = 8 * (ln + T * j), n = min(8, a.C - i);  // elements of this chunk (<= 0: none)
-            const bool vec = a.vec && n == 8;
+            const int i = first(ln, j), n = have(i);
+            const bool vec = !ANY && n == 8;
             u[j].zero();
             if (n <= 0) continue;
-            u[j].load(a.u, row * a.us + i, n, vec);
+            u[j].load(a.u, a.udt, row * a.us, i, n, T, vec);
             if constexpr (EARLY) {
-                if (a.r) r[j].load(a.r, row * a.rs + i, n, vec);
-                if (a.gate) g[j].load(a.gate, row * a.gs + i, n, vec);
+                if (a.r) r[j].load(a.r, a.rdt, row * a.rs, i, n, T, vec);
+                if (a.gate) g[j].load(a.gate, a.wdt, row * a.gs, i, n, T, vec);
             }
             if constexpr (NV == 1) {
-                if (a.post) po[0].load(a.post, i, n, vec);
-                if (a.pre) pr[0].load(a.pre, i, n, vec);
+                if (a.post) po[0].load(a.post, a.wdt, 0, i, n, T, vec);
+                if (a.pre) pr[0].load(a.pre, a.wdt, 0, i, n, T, vec);
             }
         }
         float s = a.branch;
@@ -179,37 +232,40 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q = fmaf(u[j][e], u[j][e], q);
+                for (int e = 0; e < 8; ++e) q = fmaf(u[j].at(e, a.udt), u[j].at(e, a.udt), q);
             q = row_reduce<W, false>(q, s_red[turn][0]);
             s *= 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_post);
         }
         float y[NV][8], q = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = 8 * (ln + T * j), n = min(8, a.C - i);
-            const bool vec = a.vec && n == 8;
+            const int i = first(ln, j), n = have(i);
+            const bool vec = !ANY && n == 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[j][e] = u[j][e] * s;
+            for (int e = 0; e < 8; ++e) y[j][e] = u[j].at(e, a.udt) * s;
             if (n > 0) {
                 constexpr int one = 0;
                 if (a.post) {
-                    if constexpr (NV > 1) po[0].load(a.post, i, n, vec);
+                    if constexpr (NV > 1) po[0].load(a.post, a.wdt, 0, i, n, T, vec);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[j][e] *= po[0][e];
+                    for (int e = 0; e < 8; ++e) y[j][e] *= po[0].at(e, a.wdt);
                 }
                 if (a.gate) {
                     const int k = EARLY ? j : one;
-                    if constexpr (!EARLY) g[0].load(a.gate, row * a.gs + i, n, vec);
+                    if constexpr (!EARLY) g[0].load(a.gate, a.wdt, row * a.gs, i, n, T, vec);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[j][e] *= g[k][e];
+                    for (int e = 0; e < 8; ++e) y[j][e] *= g[k].at(e, a.wdt);
                 }
                 if (a.r) {
                     const int k = EARLY ? j : one;
-                    if constexpr (!EARLY) r[0].load(a.r, row * a.rs + i, n, vec);
+                    if constexpr (!EARLY) r[0].load(a.r, a.rdt, row * a.rs, i, n, T, vec);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[j][e] = fmaf(a.res, r[k][e], y[j][e]);
+                    for (int e = 0; e < 8; ++e) y[j][e] = fmaf(a.res, r[k].at(e, a.rdt), y[j][e]);
                 }
-                if (a.ro) norm_store(a.ro, RDT, row * a.ros + i, n, vec, y[j]);
+                if (a.ro) {
+                    if constexpr (ANY) norm_store_any(a.ro, a.rdt, row * a.ros, i, n, T, y[j]);
+                    else norm_store(a.ro, RDT, row * a.ros + i, n, vec, y[j]);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) q = fmaf(y[j][e], y[j][e], q);
@@ -219,11 +275,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
             const float f = 1.0f / sqrtf(q / static_cast<float>(a.C) + a.eps_pre);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int i = 8 * (ln + T * j), n = min(8, a.C - i);
+                const int i = first(ln, j), n = have(i);
                 if (n <= 0) continue;
-                if constexpr (NV > 1) pr[0].load(a.pre, i, n, a.vec && n == 8);
+                if constexpr (NV > 1) pr[0].load(a.pre, a.wdt, 0, i, n, T, !ANY && n == 8);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[j][e] = y[j][e] * f * pr[0][e];
+                for (int e = 0; e < 8; ++e) y[j][e] = y[j][e] * f * pr[0].at(e, a.wdt);
             }
         }
         if (a.odt == BITQ_DT_ROW8) {  // the arithmetic of the activation quantizer
@@ -242,8 +298,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = 8 * (ln + T * j), n = min(8, a.C - i);
-            if (n > 0) norm_store(a.h, a.odt, row * a.hs + i, n, a.vec && n == 8, y[j]);
+            const int i = first(ln, j), n = have(i);
+            if constexpr (ANY) norm_store_any(a.h, a.odt, row * a.hs, i, n, T, y[j]);
+            else if (n > 0) norm_store(a.h, a.odt, row * a.hs + i, n, n == 8, y[j]);
         }
     }
 }
@@ -253,7 +310,11 @@ static void launch_norm(const NormArgs& a, hipStream_t st) {
     constexpr int rpb = W == 1 ? 4 : 1;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((a.M + rpb - 1) / rpb, 1 << 16)));
     const dim3 block(W == 1 ? 256 : 64 * W);
-    constexpr int F = BITQ_DT_F32, B = BITQ_DT_BF16;
+    constexpr int F = BITQ_DT_F32, B = BITQ_DT_BF16, X = kAnyType;
+    if (!a.vec) {
+        hipLaunchKernelGGL((block_norm_kernel<W, NV, X, X, X>), grid, block, 0, st, a);
+        return;
+    }
     switch ((a.udt == B) * 4 + (a.rdt == B) * 2 + (a.wdt == B)) {
         case 0: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, F, F>), grid, block, 0, st, a); break;
         case 1: hipLaunchKernelGGL((block_norm_kernel<W, NV, F, F, B>), grid, block, 0, st, a); break;

@@ -448,7 +448,7 @@ def host(t, dt):
 
 @pytest.mark.parametrize("M,C", [(1, 1), (1, 4096), (3, 7), (5, 64), (2, 513), (4, 1000), (1, 11008), (3, 28672), (2, 32768),
                                  (2, 32767), (1300, 96), (1100, 2048), (1030, 4104), (70, 8192),
-                                 (1100, 1000), (300, 4000)])
+                                 (1100, 1000), (300, 4000), (300, 4001), (300, 8001), (3, 5001), (3, 12345)])
 @pytest.mark.parametrize("udt,rdt,wdt,odt,post,gate,resid", [
     ("f", "f", "f", "f", True, "channel", True),
     ("b", "b", "b", "b", True, "token", True),
