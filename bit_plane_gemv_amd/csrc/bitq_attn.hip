@@ -457,9 +457,10 @@ __device__ __forceinline__ int first_above32(const int32_t* a, int n, int x) {
 // A range that covers an item whole writes its output; the ends of an item
 // that lies in several ranges go to the workgroup's two partial results (slot
 // 0: an item begun elsewhere, slot 1: one begun here) for the join kernel.
-template <int KVT, int NC, bool HI, bool SPLIT>
-__global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) void paged_attn_kernel(AttnArgs a) {
-    constexpr int Dp = 32 * NC, W = kAttnWaves, ROW = Dp + 4;
+template <int KVT, int NC, bool HI, bool SPLIT, int W>
+__global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, HI) * kAttnWaves / W) void paged_attn_kernel(AttnArgs a) {
+    constexpr int Dp = 32 * NC, ROW = Dp + 4;
+    static_assert(!SPLIT || W == kAttnWaves, "a unit is a pass of kAttnWaves waves");
     __shared__ __align__(16) float s_o[W][16 * ROW];
     __shared__ float s_m[W][16], s_l[W][16];
     constexpr int NQ = HI ? 3 : 1, QP = (2 * Dp + 64 * W - 1) / (64 * W);
@@ -585,7 +586,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) v
         int pg[3];
         const int from = wave_uniform(s0) + 32 * wave, upto = wave_uniform(s1);
         w.range(r, hk, wave_uniform(lo), wave_uniform(hi));
-        w.first(from, upto, kAttnUnit, L, pg);
+        w.first(from, upto, 32 * W, L, pg);
         // ---- into LDS as the terms and in the order of the operands
 #pragma unroll
         for (int u = 0; u < QP; ++u) {
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, attn_groups_per_cu(KVT, NC, HI)) v
         }
         __syncthreads();
         w.begin();
-        w.run(from, upto, kAttnUnit, L, pg);
+        w.run(from, upto, 32 * W, L, pg);
         w.park(s_o[wave], s_m[wave], s_l[wave]);
         __syncthreads();
         float* part = SPLIT ? a.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (16 * (Dp + 2)) : nullptr;
@@ -771,12 +772,13 @@ static void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 
 template <int KVT, int NC, bool HI>
 static void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * kAttnWaves);
+    const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * p.waves);
     if (!p.split) {
-        hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false>), grid, block, 0, st, a);
+        if (p.waves == 1) hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false, 1>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false, kAttnWaves>), grid, block, 0, st, a);
         return;
     }
-    hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, true>), grid, block, 4 * (static_cast<size_t>(a.R) + 1), st, a);
+    hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, true, kAttnWaves>), grid, block, 4 * (static_cast<size_t>(a.R) + 1), st, a);
     launch_join<(NC + 1) / 2>(a, p, st);
 }
 

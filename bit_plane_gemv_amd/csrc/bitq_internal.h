@@ -207,6 +207,7 @@ struct AttnPlan {
     int Dp, group, tiles;  // padded row, query heads per key-value head, 16-head tiles of them
     int items;             // requests x key-value heads x tiles
     int grid;              // workgroups of the main kernel
+    int waves;             // and their waves
     bool split;            // tokens split over workgroups and joined by a second kernel
     size_t off_part, ws_bytes;
 };

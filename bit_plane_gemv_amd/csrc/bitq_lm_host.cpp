@@ -132,6 +132,13 @@ AttnPlan attn_plan(const bitq_attn_desc& d) {
     // workgroup measured slower: one request of 2049 tokens 17.5 against 15.1 us)
     const int64_t all = p.items * units, full = 256 * attn_groups_per_cu(d.kv.dtype, p.Dp / 32, hi);
     p.grid = p.split ? static_cast<int>(std::min(full, all)) : p.items;
+    // Short spans of more items than workgroups fit at once: workgroups of one
+    // wave, of which four times as many do.  Measured, 2048 items of up to 32 /
+    // 64 / 128 tokens, bf16, us with 1 and 4 waves: rows of 128 8.6 and 12.8 /
+    // 11.8 and 13.8 / 16.7 and 15.7; of 256 21 and 43 / 26 and 45 / 39 and 54;
+    // 512 items with rows of 128 (all fit) 6.1 and 5.4 / 6.9 and 5.6.
+    const bool one = !p.split && p.items > full && (span <= 64 || full == 256);
+    p.waves = one ? 1 : kAttnWaves;
     if (p.split) {
         // prefix sums of the requests' units, then two partial results per workgroup: 16 heads x (Dp + 2) floats
         p.off_part = align256(4 * (static_cast<size_t>(d.requests) + 1));

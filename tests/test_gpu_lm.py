@@ -309,6 +309,11 @@ ATTN = [
     (1, 1, 3, 64, 64, [70000], False, True, True, 0),               # hundreds of partial results for each head
     (17, 1, 1, 64, 32, [100000] + [1] * 16, True, True, True, 0),
     (600, 1, 1, 40, 16, [20000, 0, 3] * 2 + [1] * 594, False, False, True, 0),
+    (400, 2, 3, 64, 16, [7 * i % 65 for i in range(400)], False, True, True, 0),    # workgroups of one wave
+    (260, 2, 17, 128, 16, [11 * i % 50 for i in range(260)], True, False, False, 20),
+    (150, 2, 2, 256, 32, [13 * i % 129 for i in range(150)], False, False, True, 0),
+    (300, 1, 1, 250, 8, [5 * i % 129 for i in range(300)], True, True, False, 0),
+    (5000, 1, 1, 32, 8, [3 * i % 40 for i in range(5000)], False, False, False, 0),
 ]
 
 
