@@ -381,25 +381,31 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(GemmArgs g, int tiles_m,
 }
 
 // Which kernel takes a call.  Measured on MI355X, weights from HBM, us:
-//   1 token; one channel tile a workgroup and 16 waves with rings of 3 / four
-//     tiles, 8 waves, rings of 2 / one tile, 4 waves, rings of 5:
-//       N = 2000, K = 4096    3.4 /  4.9 /  3.1
-//       4096, 4096            4.6 /  6.0 /  5.0   (3.7 TB/s of weights)
-//       4096, 11008           8.9 / 13.2 /  8.9   (5.1)
-//       6000, 4096            7.5 /  7.4 /  7.1
-//       11008, 4096          11.2 /  9.6 / 11.9   (4.7)
-//       28672, 8192          44.6 / 47.3 / 40.7   (5.8)
-//     so the first while every workgroup has a CU of its own (N <= 4096), the
-//     second while four tiles do that (N <= 16384), the third beyond.
+//   1 or 2 tokens: one channel tile a workgroup and 16 waves with rings of 3
+//     / two tiles, 8 waves, rings of 3 / four, 8, 2 / one, 4, 5:
+//       N = 4096, K = 4096    4.6 /  5.1 /  6.0 /  5.0   (3.7 TB/s of weights)
+//       4096, 11008           8.9 /  9.4 / 13.2 /  8.9   (5.1)
+//       5120, 5120            7.8 /  6.1 /  7.4 /  7.2   (4.3)
+//       5120, 13824          18.2 / 15.1 / 22.4 / 17.3   (4.7)
+//       8192, 8192           13.0 / 18.1 / 12.0 / 12.7   (5.6)
+//       11008, 4096          11.2 / 11.6 /  9.6 / 11.9   (4.7)
+//       11008, 8192          19.6 / 25.3 / 19.3 / 18.5   (4.9)
+//       28672, 8192          44.6 / 55.2 / 47.3 / 40.7   (5.8)
+//     so the first up to 4096 channels, the second up to 8192 but where rows
+//     are a multiple of 8192 apart (its workgroups then meet on the same
+//     memory channels), the third up to 16384 if k is short, else the fourth.
 //   16 tokens: a ring of 16 waves does not fit with their 2 KiB of tokens a
-//     unit; one tile and 8 waves with rings of 4 instead, 5.6 / 6.5 / 6.3 at
-//     4096 x 4096, and 13.6 / 9.7 / 13.0 at 11008 x 4096, 54.2 / 48.1 / 46.5
-//     at 28672 x 8192.
+//     unit; one tile and 8 waves with rings of 4 instead, 5.6 against 6.3 with
+//     the fourth at 4096 x 4096; 11008 x 4096 9.7 with the third, 13.0 with
+//     the fourth; 28672 x 8192 48.1 and 46.5.
 //   24 tokens: few-token kernel 16.4 against 64 x 64 tiles 11.6 at N = 11008,
 //     12.1 against 13.7 (4 k ranges) at N = 4096, K = 11008
 //   40 tokens: 19.2 against 11.8; 14.7 against 14.2
 //   64 tokens: 21.2 against 15.3; 17.9 against 14.6 (K = 11008); 8.3 against
 //     9.6 (4096 x 4096)
+//   k = 16384, against 64 x 64 tiles with their ranges of k: 24 tokens 13.0 and
+//     11.7 at N = 2048, 40 tokens 11.5 and 10.2 at N = 1024; k = 11008, N = 2048,
+//     24 tokens 8.0 and 10.8
 // So the few-token kernel keeps up to 16 tokens, and up to 64 when there are
 // too few channels for a tile on every CU and k is short enough.
 // Tiles: 64 x 64, 64 x 128, 128 x 128, 256 x 256 with k ranges of 4096 take
@@ -410,14 +416,15 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(GemmArgs g, int tiles_m,
 // 16.4, 128 x 128 19.1; 256: 64 x 64 11.6, 64 x 128 13.5.)
 // Too few 64 x 64 tiles for the CUs and a long k: the k range is split and
 // joined by a second kernel, which costs about 4 us (M = 64, 4096 x 11008:
-// 23.0 -> 14.6 us with 4 ranges; 64 x 28672: 87 -> 28.8; at K = 4096 and 64
-// tiles it gains nothing).
+// 23.0 -> 14.6 us with 4 ranges; at K = 4096 and 64 tiles it gains nothing).
+// Up to 8 ranges where there are few tiles: 64 x 1024 x 28672 47 us whole, 17.9
+// with 4, 12.8 with 8; 128 x 256 x 16384 27.6, 12.1, 9.5.
 enum { kTile64 = 5, kTile64x128 = 6, kTile128 = 7, kTile256 = 8 };
 
 W8A8Plan w8a8_plan(const bitq_w8a8_desc& d) {
     W8A8Plan p{};
     p.splits = 1;
-    if (d.M <= 16 || (d.M <= 64 && d.N <= 6144 && (d.M <= 48 || d.K <= 6144))) {
+    if (d.M <= 16 || (d.M <= 64 && d.N <= 6144 && d.K <= (d.M <= 48 ? 12288 : 6144))) {
         p.kernel = (d.M + 15) / 16;
         return p;
     }
@@ -432,7 +439,7 @@ W8A8Plan w8a8_plan(const bitq_w8a8_desc& d) {
     for (int i = 1; i < 4; ++i)
         if (us[i] < us[p.kernel - kTile64]) p.kernel = kTile64 + i;
     if (p.kernel == kTile64 && t64 <= 128 && (d.K >= 6144 || (t64 <= 32 && d.K >= 4096))) {
-        p.splits = static_cast<int>(std::min<int64_t>({4, 256 / t64, d.K / 1024}));
+        p.splits = static_cast<int>(std::min<int64_t>({8, 256 / t64, d.K / 1024}));
         p.ws_bytes = static_cast<size_t>(p.splits) * t64 * 64 * 64 * 4;
     }
     return p;
@@ -471,7 +478,8 @@ int launch_gemm_w8a8(const bitq_w8a8_desc& d, const W8A8Plan& plan, const void* 
     switch (plan.kernel) {
         case 1:
             if (d.N <= 4096) return d.M <= 8 ? launch_few<1, 1, 16, 3, 1>(g, st) : launch_few<1, 1, 8, 4>(g, st);
-            if (d.N <= 16384) return launch_few<1, 4, 8, 2>(g, st);
+            if (d.N <= 8192 && d.ldw % 8192) return launch_few<1, 2, 8, 3>(g, st);
+            if (d.N > 8192 && d.N <= 16384 && d.K <= 6144) return launch_few<1, 4, 8, 2>(g, st);
             return launch_few<1, 1, 4, 5>(g, st);
         case 2: return launch_few<2, 1, 8, 3>(g, st);
         case 3: return launch_few<3, 1, 8, 2>(g, st);

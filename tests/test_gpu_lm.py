@@ -557,7 +557,8 @@ W8A8 = [(1, 1, 16), (1, 16, 64), (1, 17, 4096), (2, 100, 80), (16, 33, 144), (17
         (64, 300, 512), (49, 4096, 1024), (65, 129, 128), (100, 257, 400), (128, 128, 128), (129, 300, 1040), (200, 512, 4096),
         (257, 1000, 656), (300, 16, 16), (1000, 777, 2000), (513, 2049, 272), (5, 20, 131056), (130, 140, 131056),
         (9, 3000, 1040), (16, 9001, 272), (20, 7000, 528), (64, 300, 6160), (70, 1500, 7008), (520, 8100, 208), (3000, 9100, 80),
-        (2500, 3000, 336), (64, 64, 6400), (7, 4095, 8224), (8, 600, 2064), (11, 4097, 144), (3, 17001, 656), (12, 16400, 272)]
+        (2500, 3000, 336), (64, 64, 6400), (7, 4095, 8224), (8, 600, 2064), (11, 4097, 144), (3, 17001, 656), (12, 16400, 272),
+        (2, 5000, 8192), (16, 8192, 400), (4, 9000, 6160), (600, 60, 8480), (30, 100, 14352), (64, 200, 12304)]
 
 
 @pytest.mark.parametrize("M,N,K", W8A8)
