@@ -163,11 +163,14 @@ __global__ __launch_bounds__(64 * KW) void w8a8_few_kernel(GemmArgs g) {
 // Tiles of BM tokens x BN channels in a ring of NS stages of KSUB units of k;
 // wave tiles of WM x WN.  The copies run NS - 1 stages ahead, the operand
 // reads one unit ahead of the products (a second set of operand registers),
-// and the workgroup meets once per stage.  Bound by the matrix cores and the
-// power they may draw where there are many tokens (4096 x 11008 x 4096: 164 -
-// 178 us, 2.1 - 2.25 POP/s, matrix cores busy 69 % of the cycles at 1.8 GHz),
-// by the weight stream and the ramp of its few workgroups otherwise (64 x 4096
-// x 11008: 10 us and the join's 4).
+// and the workgroup meets once per stage.  Many tokens: bound by the matrix
+// cores and LDS, which a 256 x 256 tile loads alike (1024 cycles of products,
+// 768 of operand reads and 256 of copies per unit), at the clock that their
+// power allows: 4096 x 8192 x 8192 231 us, 2.38 POP/s, what a library product
+// of 8192^3 reaches; 4096 x 11008 x 4096 164 - 180 us, 2.05 - 2.25 POP/s, its
+// 688 tiles filling 2.7 of 3 rounds.  (Waves of 128 x 128, with fewer operand
+// reads, but one to a SIMD: 198 us.)  Few tokens: bound by the weight stream
+// and the ramp of its few workgroups (64 x 4096 x 11008: 10 us and the join's 4).
 //
 // The tile's outputs go through LDS, a wave's part of it at a time, and leave
 // as 16-byte stores of whole 128-byte lines.
