@@ -314,6 +314,8 @@ ATTN = [
     (150, 2, 2, 256, 32, [13 * i % 129 for i in range(150)], False, False, True, 0),
     (300, 1, 1, 250, 8, [5 * i % 129 for i in range(300)], True, True, False, 0),
     (5000, 1, 1, 32, 8, [3 * i % 40 for i in range(5000)], False, False, False, 0),
+    (4096, 1, 1, 256, 8, [300] + [i % 4 for i in range(4095)], False, True, True, 0),   # the most LDS: sums of 4096 requests
+    (4097, 1, 2, 64, 16, [300] + [i % 4 for i in range(4096)], True, False, False, 0),  # too many of them: one workgroup an item
 ]
 
 
