@@ -127,7 +127,16 @@ AttnPlan attn_plan(const bitq_attn_desc& d) {
     const int64_t span = d.window > 0 ? std::min<int64_t>(d.max_len, static_cast<int64_t>(d.window) + 31) : d.max_len;
     const int64_t units = (span + kAttnUnit - 1) / kAttnUnit;  // of the longest request
     const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
-    p.split = units > 1 && d.requests <= kAttnMaxSplitRequests && p.items * units < INT32_MAX;
+    // A workgroup for each item while the longest is short: the split's second
+    // kernel costs about 4 us, a unit of an item 0.6 us and more with its row.
+    // Where items fill half of the CUs and more the others' work hides it.
+    // Measured, bf16, whole / split, us: 16 items with rows of 128, 512 tokens
+    // 7.9 / 9.5, 1024 12.4 / 10.0; rows of 64, 1024 8.8 / 8.9; of 256, 256 tokens
+    // 9.0 / 11.6, 512 13.3 / 11.9.  128 items, rows of 128, 1024 tokens 15.1 /
+    // 17.8, 2048 31.5 / 31.7; of 256, 512 15.9 / 18.4, 1024 33 / 32.  2048 items
+    // of up to 256 ragged tokens 30 / 41.
+    const bool whole = units <= 8 && units * p.Dp <= (p.items >= 128 ? 1024 : 640);
+    p.split = !whole && d.requests <= kAttnMaxSplitRequests && p.items * units < INT32_MAX;
     // (the CUs filled as often as registers allow; two units and more for a
     // workgroup measured slower: one request of 2049 tokens 17.5 against 15.1 us)
     const int64_t all = p.items * units, full = 256 * attn_groups_per_cu(d.kv.dtype, p.Dp / 32, hi);

@@ -316,6 +316,14 @@ ATTN = [
     (5000, 1, 1, 32, 8, [3 * i % 40 for i in range(5000)], False, False, False, 0),
     (4096, 1, 1, 256, 8, [300] + [i % 4 for i in range(4095)], False, True, True, 0),   # the most LDS: sums of 4096 requests
     (4097, 1, 2, 64, 16, [300] + [i % 4 for i in range(4096)], True, False, False, 0),  # too many of them: one workgroup an item
+    (4096, 1, 1, 256, 8, [1500] + [i % 4 for i in range(4095)], False, True, True, 0),
+    (4097, 1, 2, 64, 16, [1500] + [i % 4 for i in range(4096)], True, False, False, 0),
+    (64, 2, 4, 128, 16, "long", False, False, False, 0),            # long enough to be split
+    (65, 2, 4, 128, 16, "long", True, True, True, 0),
+    (64, 1, 4, 88, 16, "long", True, True, False, 1300),
+    (70, 4, 2, 64, 16, "long", False, False, True, 1100),
+    (30, 3, 20, 96, 32, "long", False, False, False, 0),
+    (140, 1, 3, 160, 64, "long", True, False, True, 0),
 ]
 
 
@@ -328,6 +336,9 @@ def test_attention(R, H, G, D, page, lens, int8, qf32, of32, window):
         lens[[3, 4]] = 0, 900
     elif lens == "short":
         lens = rng.integers(0, 140, R)
+    elif lens == "long":
+        lens = (rng.random(R) ** 3 * 3000).astype(int)
+        lens[[3, 4]] = 0, 3000
     K, V, ks, vs, q, table = attention_case(rng, R, H, G, D, page, lens, int8, qf32, 2.0)
     max_len = max(1, max(lens))
     scale = D ** -0.5
