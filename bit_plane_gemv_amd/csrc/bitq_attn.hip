@@ -38,9 +38,12 @@ namespace bitq {
 //
 // Precision.  bf16 and int8 cache rows are exact in bf16; int8 scales are
 // applied in fp32, to the scores and to p.  fp32 q is split into 3 bf16
-// terms (exact), bf16 q needs one.  p is split into 2 terms (relative
-// rounding 2^-17, below half an ulp of a bf16 output) or, when q or the output is
-// fp32, into 3 (2^-25).  Everything else is fp32.
+// terms, which hold its 24 bits, bf16 q needs one.  p (times V's scale) is
+// split into 3 terms alike: 2 (2^-17) would change the rounding of one bf16
+// output in a thousand over a long context and save nothing there (bf16 rows;
+// int8, 64 ragged requests of up to 4096 tokens, us with 2 and 3: rows of 64
+// 41.7 and 43.5, 128 71.5 and 72.6, 256 123 and 124).  Everything else is
+// fp32.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
@@ -57,7 +60,7 @@ struct AttnArgs {
     size_t off_v, off_ks, off_vs;
     int R, H, A, group, tiles, D, page_shift, pages, table_stride, max_len, window;
     float c;           // scale log2(e): p = 2^(c s - m)
-    int qdt, odt;
+    int odt;
     int qvec;          // 16-byte loads of q: D a multiple of 8, rows and base aligned
 };
 
@@ -134,11 +137,11 @@ struct AttnStep {
     float4 ks[KVT == BITQ_KV_INT8 ? 2 : 1], vs[KVT == BITQ_KV_INT8 ? 2 : 1];
 };
 
-template <int KVT, int NC, bool HI>
+template <int KVT, int NC, bool Q32>
 struct AttnWave {
-    static constexpr int NQ = HI ? 3 : 1, NP = HI ? 3 : 2, Dp = 32 * NC;
+    static constexpr int NQ = Q32 ? 3 : 1, NP = 3, Dp = 32 * NC;
     static constexpr bool I8 = KVT == BITQ_KV_INT8;
-    bf16x8_t q[HI ? 1 : NC];  // bf16 q: the operands; else they are read from LDS where they are used
+    bf16x8_t q[Q32 ? 1 : NC];  // bf16 q: the operands; else they are read from LDS where they are used
     f32x4_t o[2 * NC];
     float m, l;
     const AttnArgs& a;
@@ -162,7 +165,7 @@ struct AttnWave {
         row = a.table + static_cast<size_t>(r) * a.table_stride;
     }
     __device__ __forceinline__ void begin() {
-        if constexpr (!HI) {
+        if constexpr (!Q32) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) q[c] = q_operand(0, c);
         }
@@ -252,7 +255,7 @@ struct AttnWave {
                 }
 #pragma unroll
                 for (int n = NQ - 1; n >= 0; --n)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, HI ? q_operand(n, c) : q[HI ? 0 : c], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, Q32 ? q_operand(n, c) : q[Q32 ? 0 : c], acc, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[4 * t + i] = acc[i];
@@ -457,19 +460,19 @@ __device__ __forceinline__ int first_above32(const int32_t* a, int n, int x) {
 // A range that covers an item whole writes its output; the ends of an item
 // that lies in several ranges go to the workgroup's two partial results (slot
 // 0: an item begun elsewhere, slot 1: one begun here) for the join kernel.
-template <int KVT, int NC, bool HI, bool SPLIT, int W>
-__global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, HI) * kAttnWaves / W) void paged_attn_kernel(AttnArgs a) {
+template <int KVT, int NC, bool Q32, bool SPLIT, int W>
+__global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, Q32) * kAttnWaves / W) void paged_attn_kernel(AttnArgs a) {
     constexpr int Dp = 32 * NC, ROW = Dp + 4;
     static_assert(!SPLIT || W == kAttnWaves, "a unit is a pass of kAttnWaves waves");
     __shared__ __align__(16) float s_o[W][16 * ROW];
     __shared__ float s_m[W][16], s_l[W][16];
-    constexpr int NQ = HI ? 3 : 1, QP = (2 * Dp + 64 * W - 1) / (64 * W);
+    constexpr int NQ = Q32 ? 3 : 1, QP = (2 * Dp + 64 * W - 1) / (64 * W);
     __shared__ __align__(16) __bf16 s_q[NQ * 16 * Dp];
     extern __shared__ int32_t s_pre[];  // SPLIT: [R + 1]
     __shared__ int32_t s_scan[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int HT = a.H * a.tiles;
-    AttnWave<KVT, NC, HI> w(a, lane, s_q);
+    AttnWave<KVT, NC, Q32> w(a, lane, s_q);
 
     int x = blockIdx.x, x1 = x + 1;  // units (SPLIT; fewer than 2^31) or the item
     int U = 1;
@@ -559,17 +562,16 @@ __global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, HI) * kAttnWave
         const int heads = min(16, a.group - 16 * tile);
         // ---- the tile's queries, 8 elements of a head at a time; then the first step's loads, behind them
         const int64_t qat = static_cast<int64_t>(r) * a.q_stride + (static_cast<int64_t>(hk) * a.group + 16 * tile) * a.D;
-        const bool q32 = HI && a.qdt == BITQ_DT_F32;
         uint32_t qv[QP][8];
 #pragma unroll
         for (int u = 0; u < QP; ++u) {
             const int i = tid + 64 * W * u, head = min(i / (Dp / 8), heads - 1), d = 8 * (i % (Dp / 8));
             // (as loaded: a conversion here would wait for the loads)
             if (a.qvec) {
-                const uint8_t* p = static_cast<const uint8_t*>(a.q) + (qat + head * a.D + min(d, a.D - 8)) * (q32 ? 4 : 2);
+                const uint8_t* p = static_cast<const uint8_t*>(a.q) + (qat + head * a.D + min(d, a.D - 8)) * (Q32 ? 4 : 2);
                 const uint4 v0 = reinterpret_cast<const uint4*>(p)[0];
                 qv[u][0] = v0.x, qv[u][1] = v0.y, qv[u][2] = v0.z, qv[u][3] = v0.w;
-                if (q32) {
+                if (Q32) {
                     const uint4 v1 = reinterpret_cast<const uint4*>(p)[1];
                     qv[u][4] = v1.x, qv[u][5] = v1.y, qv[u][6] = v1.z, qv[u][7] = v1.w;
                 }
@@ -577,7 +579,7 @@ __global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, HI) * kAttnWave
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t at = head * a.D + min(d + e, a.D - 1);
-                    if (q32) qv[u][e] = (static_cast<const uint32_t*>(a.q) + qat)[at];
+                    if (Q32) qv[u][e] = (static_cast<const uint32_t*>(a.q) + qat)[at];
                     else qv[u][e] = (static_cast<const uint16_t*>(a.q) + qat)[at];
                 }
             }
@@ -596,7 +598,7 @@ __global__ __launch_bounds__(64 * W, attn_groups_per_cu(KVT, NC, HI) * kAttnWave
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t pair = qv[u][e / 2];
-                const uint32_t bits = q32 ? qv[u][e] : !a.qvec ? qv[u][e] << 16 : e & 1 ? pair & 0xFFFF0000u : pair << 16;
+                const uint32_t bits = Q32 ? qv[u][e] : !a.qvec ? qv[u][e] << 16 : e & 1 ? pair & 0xFFFF0000u : pair << 16;
                 f[e] = head < heads && d + e < a.D ? __uint_as_float(bits) : 0.0f;
             }
             bf16x8_t t[NQ];
@@ -770,29 +772,29 @@ static void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
         hipLaunchKernelGGL((attn_join_kernel<16, NE>), dim3(heads), dim3(1024), 0, st, a, p.Dp, p.grid);
 }
 
-template <int KVT, int NC, bool HI>
+template <int KVT, int NC, bool Q32>
 static void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * p.waves);
     if (!p.split) {
-        if (p.waves == 1) hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false, 1>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, false, kAttnWaves>), grid, block, 0, st, a);
+        if (p.waves == 1) hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, Q32, false, 1>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, Q32, false, kAttnWaves>), grid, block, 0, st, a);
         return;
     }
-    hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, HI, true, kAttnWaves>), grid, block, 4 * (static_cast<size_t>(a.R) + 1), st, a);
+    hipLaunchKernelGGL((paged_attn_kernel<KVT, NC, Q32, true, kAttnWaves>), grid, block, 4 * (static_cast<size_t>(a.R) + 1), st, a);
     launch_join<(NC + 1) / 2>(a, p, st);
 }
 
-template <int KVT, bool HI>
+template <int KVT, bool Q32>
 static void launch_attn_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     switch (p.Dp / 32) {
-        case 1: launch_attn<KVT, 1, HI>(a, p, st); break;
-        case 2: launch_attn<KVT, 2, HI>(a, p, st); break;
-        case 3: launch_attn<KVT, 3, HI>(a, p, st); break;
-        case 4: launch_attn<KVT, 4, HI>(a, p, st); break;
-        case 5: launch_attn<KVT, 5, HI>(a, p, st); break;
-        case 6: launch_attn<KVT, 6, HI>(a, p, st); break;
-        case 7: launch_attn<KVT, 7, HI>(a, p, st); break;
-        default: launch_attn<KVT, 8, HI>(a, p, st); break;
+        case 1: launch_attn<KVT, 1, Q32>(a, p, st); break;
+        case 2: launch_attn<KVT, 2, Q32>(a, p, st); break;
+        case 3: launch_attn<KVT, 3, Q32>(a, p, st); break;
+        case 4: launch_attn<KVT, 4, Q32>(a, p, st); break;
+        case 5: launch_attn<KVT, 5, Q32>(a, p, st); break;
+        case 6: launch_attn<KVT, 6, Q32>(a, p, st); break;
+        case 7: launch_attn<KVT, 7, Q32>(a, p, st); break;
+        default: launch_attn<KVT, 8, Q32>(a, p, st); break;
     }
 }
 
@@ -825,17 +827,16 @@ int launch_paged_attn(const bitq_attn_desc& d, const AttnPlan& plan, const void*
     a.max_len = d.max_len;
     a.window = d.window;
     a.c = d.scale * 1.44269504088896340736f;
-    a.qdt = d.q_dtype;
     a.odt = d.out_dtype;
     const int per16 = d.q_dtype == BITQ_DT_F32 ? 4 : 8;
     a.qvec = a.D % 8 == 0 && q_stride % per16 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    const bool q32 = d.q_dtype == BITQ_DT_F32;
     if (d.kv.dtype == BITQ_KV_BF16) {
-        if (hi) launch_attn_dim<BITQ_KV_BF16, true>(a, plan, st);
+        if (q32) launch_attn_dim<BITQ_KV_BF16, true>(a, plan, st);
         else launch_attn_dim<BITQ_KV_BF16, false>(a, plan, st);
     } else {
-        if (hi) launch_attn_dim<BITQ_KV_INT8, true>(a, plan, st);
+        if (q32) launch_attn_dim<BITQ_KV_INT8, true>(a, plan, st);
         else launch_attn_dim<BITQ_KV_INT8, false>(a, plan, st);
     }
     return static_cast<int>(hipGetLastError());

@@ -193,15 +193,15 @@ inline KvPlanLayout kv_plan_layout(const bitq_kv_plan_desc& d) {
 constexpr int kAttnWaves = 4;                    // waves per workgroup
 constexpr int kAttnUnit = 32 * kAttnWaves;       // tokens a workgroup takes per pass
 constexpr int kAttnMaxSplitRequests = 4096;      // the split kernel keeps their prefix sums in LDS
-// Workgroups per CU of the kernel for rows of 32 nc elements (hi: fp32 q or
-// output): as many as hide the memory's latency, and no more than registers
-// allow without spilling in the loop.  Measured, 64 ragged requests of up to
+// Workgroups per CU of the kernel for rows of 32 nc elements (q32: fp32 q):
+// as many as hide the memory's latency, and no more than registers allow
+// without spilling in the loop.  Measured, 64 ragged requests of up to
 // 4096 tokens, 64 heads on 8, us: bf16 rows of 96 88 with 2 and 91 with 3,
 // int8 rows of 128 71 with 2 and 74 with 3, of 64 42 with 4 and 46 with 3;
 // bf16 rows of 64, 2 requests of 30000 tokens, 30.7 with 3 and 33.1 with 4.
-constexpr int attn_groups_per_cu(int kv_dtype, int nc, bool hi) {
-    return kv_dtype == BITQ_KV_INT8 ? (nc <= 2 ? 4 : nc == 3 ? 3 : nc <= (hi ? 6 : 7) ? 2 : 1)
-                                    : (nc <= 2 ? 3 : nc <= (hi ? 5 : 6) ? 2 : 1);
+constexpr int attn_groups_per_cu(int kv_dtype, int nc, bool q32) {
+    return kv_dtype == BITQ_KV_INT8 ? (nc <= 2 ? 4 : nc == 3 ? 3 : nc <= (q32 ? 6 : 7) ? 2 : 1)
+                                    : (nc <= 2 ? 3 : nc <= (q32 ? 5 : 6) ? 2 : 1);
 }
 struct AttnPlan {
     int Dp, group, tiles;  // padded row, query heads per key-value head, 16-head tiles of them

@@ -126,7 +126,7 @@ AttnPlan attn_plan(const bitq_attn_desc& d) {
     p.items = d.requests * d.kv.kv_heads * p.tiles;
     const int64_t span = d.window > 0 ? std::min<int64_t>(d.max_len, static_cast<int64_t>(d.window) + 31) : d.max_len;
     const int64_t units = (span + kAttnUnit - 1) / kAttnUnit;  // of the longest request
-    const bool hi = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    const bool q32 = d.q_dtype == BITQ_DT_F32;
     // A workgroup for each item while the longest is short: the split's second
     // kernel costs about 4 us, a unit of an item 0.6 us and more with its row.
     // Where items fill half of the CUs and more the others' work hides it.
@@ -139,7 +139,7 @@ AttnPlan attn_plan(const bitq_attn_desc& d) {
     p.split = !whole && d.requests <= kAttnMaxSplitRequests && p.items * units < INT32_MAX;
     // (the CUs filled as often as registers allow; two units and more for a
     // workgroup measured slower: one request of 2049 tokens 17.5 against 15.1 us)
-    const int64_t all = p.items * units, full = 256 * attn_groups_per_cu(d.kv.dtype, p.Dp / 32, hi);
+    const int64_t all = p.items * units, full = 256 * attn_groups_per_cu(d.kv.dtype, p.Dp / 32, q32);
     p.grid = p.split ? static_cast<int>(std::min(full, all)) : p.items;
     // Short spans of more items than workgroups fit at once: workgroups of one
     // wave, of which four times as many do.  Measured, 2048 items of up to 32 /
