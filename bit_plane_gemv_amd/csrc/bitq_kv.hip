@@ -303,15 +303,21 @@ struct Raw8 {
     }
 };
 
-// Scale of a row from this thread's 8 elements (LR lanes share the row), and its codes in place.
+// Scale of a row from this thread's 8 elements (LR lanes share the row), and its codes in place.  The amax is the
+// largest of the magnitudes' bits, so NaN passes as the largest of all; a product that is NaN (an infinity or NaN in the
+// row; a zero where 127 / amax overflows) has the code 0.
 __device__ __forceinline__ float row_codes(float (&v)[8], int LR) {
-    float a = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
-    for (int o = 1; o < LR; o <<= 1) a = fmaxf(a, __shfl_xor(a, o, 64));
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(fabsf(v[e])));
+    for (int o = 1; o < LR; o <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(m, o, 64)));
+    const float a = __uint_as_float(m);
     const float s = a > 0.0f ? __fdiv_rn(127.0f, a) : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(rintf(__fmul_rn(v[e], s)), -127.0f), 127.0f);
+    for (int e = 0; e < 8; ++e) {
+        const float q = rintf(__fmul_rn(v[e], s));
+        v[e] = q == q ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
+    }
     return __fdiv_rn(a, 127.0f);
 }
 

@@ -124,6 +124,8 @@ bitq_status bitq_kv_plan(const bitq_kv_plan_desc* desc, const int32_t* old_dev, 
  *                 element
  *   cache_dev     the cache, 256-byte aligned
  * bf16 caches round to nearest, ties to even; int8 caches quantize each row.
+ * An int8 row with an infinity or NaN gets that as its scale and codes 0: every
+ * value of it is NaN.
  * tokens = 0 does nothing; tokens <= 2^24, tokens * kv_heads <= 2^28.
  */
 bitq_status bitq_kv_write(const bitq_kvdesc* kv, const void* k_dev, const void* v_dev, int32_t x_dtype,
@@ -166,7 +168,8 @@ bitq_status bitq_paged_attn_workspace(const bitq_attn_desc* desc, size_t* bytes)
  *   lse_dev   f32 [R][heads] log(sum_t p_t), or NULL
  * A request without tokens gives out = 0 and lse = -inf.  Whatever the cache
  * holds outside a request's tokens, infinities and NaN included, has no
- * effect on its output.
+ * effect on its output.  NaN in its own q, keys or values gives NaN; so may an
+ * infinity there.
  */
 bitq_status bitq_paged_attn(const bitq_attn_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
                             size_t cache_bytes, const int32_t* table_dev, const int32_t* lens_dev, void* out_dev,
