@@ -167,13 +167,18 @@ __device__ __forceinline__ void norm_store_any(void* p, int dt, int64_t at, int 
     }
 }
 
-// Sum (or maximum) over the W waves of a row, in a fixed order.
+// The larger of two magnitudes, by their bits: NaN is the largest of all.
+__device__ __forceinline__ float larger(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// Sum (or largest magnitude) over the W waves of a row, in a fixed order.
 template <int W, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* s) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
         const float t = __shfl_xor(v, o, 64);
-        v = MAX ? fmaxf(v, t) : v + t;
+        v = MAX ? larger(v, t) : v + t;
     }
     if constexpr (W > 1) {  // (s: a place that no wave can still be reading)
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -181,7 +186,7 @@ __device__ __forceinline__ float row_reduce(float v, float* s) {
         __syncthreads();
         v = s[0];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v = MAX ? fmaxf(v, s[w]) : v + s[w];
+        for (int w = 1; w < W; ++w) v = MAX ? larger(v, s[w]) : v + s[w];
     }
     return v;
 }
@@ -287,14 +292,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[j][e]));
+                for (int e = 0; e < 8; ++e) m = larger(m, fabsf(y[j][e]));
             m = row_reduce<W, true>(m, s_red[turn][2]);
             const float f = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
-            if (ln == 0) a.d[row] = m > 0.0f ? __fdiv_rn(m, 127.0f) : 0.0f;
+            if (ln == 0) a.d[row] = __fdiv_rn(m, 127.0f);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[j][e] = fminf(fmaxf(rintf(__fmul_rn(y[j][e], f)), -127.0f), 127.0f);
+                for (int e = 0; e < 8; ++e) {
+                    // (NaN: an infinity or NaN in the row, whose scale says so, or a zero where 127 / m overflows)
+                    const float q = rintf(__fmul_rn(y[j][e], f));
+                    y[j][e] = q == q ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
+                }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {

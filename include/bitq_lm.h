@@ -198,7 +198,8 @@ typedef struct {
 } bitq_norm_desc;
 
 /* h in int8 rows: codes int8 [M] rows and one fp32 scale per row (the
- * arithmetic of bitq_quantize_act), what bitq_gemm_w8a8 takes. */
+ * arithmetic of bitq_quantize_act), what bitq_gemm_w8a8 takes.  A row with an
+ * infinity or NaN gets that as its scale and codes 0: every value of it is NaN. */
 #define BITQ_DT_ROW8 16
 
 /*

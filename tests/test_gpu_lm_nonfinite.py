@@ -1,4 +1,4 @@
-"""Infinities, NaN and the smallest numbers through the int8 rows of the cache write, and through
+"""Infinities, NaN and the smallest numbers through the int8 rows of the cache write and the block norm, and through
 attention: what is not finite stays so."""
 import math
 
@@ -90,3 +90,47 @@ def test_attention_over_rows_that_are_not_finite(int8, lens):
     assert np.isnan(out[bad]).all() and np.array_equal(out[~bad], clean[~bad])
     bad[1] = False                                   # (the log-sum reads no values)
     assert np.isnan(lse[bad]).all() and np.array_equal(lse[~bad], clse[~bad])
+
+
+@pytest.mark.parametrize("M,C,pad", [(9, 64, 0), (9, 61, 3), (40, 1000, 0), (1100, 1000, 0), (20, 4096, 0), (300, 4096, 0),
+                                     (300, 4097, 2), (20, 8192, 0), (20, 16384, 0), (9, 28672, 0), (9, 28673, 0)])
+@pytest.mark.parametrize("post,pre,resid,f32", [(False, False, False, True), (True, True, True, False), (False, True, True, True)])
+def test_int8_norm_keeps_what_is_not_finite(M, C, pad, post, pre, resid, f32):
+    """A row of h with an infinity or NaN stands for NaN in every element; the other rows are as they are without it."""
+    import torch
+    say("norm nonfinite", M, C, pad, post, pre, resid, f32)
+    g = torch.Generator().manual_seed(M + C)
+    t, code = (torch.float32, bq.DT_F32) if f32 else (torch.bfloat16, bq.DT_BF16)
+    f = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    u, r = f(M, C + pad).to(t), f(M, C + pad).to(t)
+    w = (1 + 0.1 * f(C)).to(t).cuda()
+    bad = torch.zeros(M, dtype=torch.bool)
+    odd = u.clone()
+    for i in range(min(M - 3, 40)):
+        m = 2 + i
+        odd[m, int(torch.randint(C, (1,), generator=g))] = ODD[i % 4]
+        bad[m] = True
+    d = bq.norm_desc(M, C, code, code, code, bq.DT_ROW8, res_scale=0.5, branch_scale=0.7, u_stride=C + pad, r_stride=C + pad,
+                     h_stride=C)
+    runs = []
+    for x in (u, odd):
+        q, s = torch.full((M, C), 99, dtype=torch.int8, device="cuda"), torch.full((M,), 7.0, device="cuda")
+        bq.block_norm(d, x.cuda(), r.cuda() if resid else None, w if post else None, None, w if pre else None, None, q, s)
+        torch.cuda.synchronize()
+        runs.append((q.cpu(), s.cpu()))
+    (q0, s0), (q, s) = runs
+    assert bool(torch.isnan(q.float() * s[:, None])[bad].all()), "a row that is not finite lost it"
+    assert torch.equal(q[~bad], q0[~bad]) and torch.equal(s[~bad], s0[~bad])
+
+
+def test_int8_norm_of_the_smallest_rows():
+    """Rows whose 127/amax overflows: zeros stay zeros."""
+    import torch
+    say("norm smallest")
+    u = torch.zeros(3, 64, device="cuda")
+    u[0, :3] = torch.tensor([1e-38, -2e-39, 1e-38])
+    u[1, 5] = -1e-40
+    q, s = torch.full((3, 64), 99, dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+    bq.block_norm(bq.norm_desc(3, 64, out_dtype=bq.DT_ROW8, branch_scale=1.0), u, None, None, None, None, None, q, s)
+    assert torch.equal(q.cpu(), (127 * torch.sign(u)).to(torch.int8).cpu())
+    assert torch.equal(s.cpu(), torch.from_numpy(np.float32([1e-38, np.float32(1e-40), 0]) / np.float32(127)))
