@@ -218,6 +218,26 @@ def _addr(x) -> int | None:
         return _ptr(x)
 
 
+# Element types of a tensor of int32 values: what else holds them would be read as something else.
+_WORDS = frozenset() if _torch is None else frozenset((_torch.int32, _torch.uint32, _torch.uint8))
+
+
+def _ints(x, n: int, name: str, stride: int = 0) -> int | None:
+    """Address of n int32 values in a row; a tensor has to hold them (a table: in rows `stride` apart)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if x.dtype not in _WORDS:
+        raise TypeError(f"{name} must be int32, not {x.dtype}")
+    if not x.is_contiguous():
+        if not stride or x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != stride or x.size(0) * stride < n:
+            raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call reads {n} values in a row")
+    elif x.numel() * x.element_size() < 4 * n:
+        raise ValueError(f"{name} has {x.numel()} values, the call needs {n}")
+    return x.data_ptr()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return _raw_stream()
@@ -478,18 +498,22 @@ def kv_plan_views(desc: KvPlanDesc, plan) -> dict:
 
 
 def kv_plan(desc: KvPlanDesc, old_len, new_len, ring, state, table, plan, stream=None):
-    """One scheduling step: pages from and to the ring, tables, slots (bitq_kv_plan)."""
-    _check(_lib.bitq_kv_plan(desc, _addr(old_len), _addr(new_len), _addr(ring), _addr(state), _addr(table), _addr(plan),
-                             _nbytes(plan), _stream(stream)))
+    """One scheduling step: pages from and to the ring, tables, slots (bitq_kv_plan).  Lengths, ring, state and table are
+    int32 (TypeError otherwise) and as many as the descriptor says (ValueError)."""
+    R, per = desc.requests, desc.table_stride
+    _check(_lib.bitq_kv_plan(desc, _ints(old_len, R, "old_len"), _ints(new_len, R, "new_len"), _ints(ring, desc.ring, "ring"),
+                             _ints(state, 2, "state"), _ints(table, R * per, "table", per), _addr(plan), _nbytes(plan),
+                             _stream(stream)))
 
 
 def kv_write(kv: KvDesc, k, v, x_dtype: int, slots, cache, tokens: int | None = None, k_stride: int | None = None,
              v_stride: int | None = None, stream=None):
     """Keys and values of new tokens into their slots (bitq_kv_write).  k, v: tensors [tokens, kv_heads,
-    head_dim] whose last two dimensions are contiguous (or addresses, with the strides given)."""
+    head_dim] whose last two dimensions are contiguous (or addresses, with the strides given); slots: int32."""
+    tokens = slots.numel() if tokens is None else tokens
     _check(_lib.bitq_kv_write(kv, _addr(k), _addr(v), x_dtype, k.stride(0) if k_stride is None else k_stride,
-                              v.stride(0) if v_stride is None else v_stride, _addr(slots),
-                              slots.numel() if tokens is None else tokens, _addr(cache), _nbytes(cache), _stream(stream)))
+                              v.stride(0) if v_stride is None else v_stride, _ints(slots, tokens, "slots"), tokens, _addr(cache),
+                              _nbytes(cache), _stream(stream)))
 
 
 def attn_desc(kv: KvDesc, heads: int, requests: int, table_stride: int, max_len: int, window: int = 0,
@@ -504,10 +528,11 @@ def paged_attn_workspace(desc: AttnDesc) -> int:
 
 def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_stride: int | None = None,
                ws_bytes: int | None = None, stream=None):
-    """Attention of one new token per request over the paged cache (bitq_paged_attn)."""
+    """Attention of one new token per request over the paged cache (bitq_paged_attn).  table and lens: int32."""
+    R, per = desc.requests, desc.table_stride
     _check(_lib.bitq_paged_attn(desc, _addr(q), q.stride(0) if q_stride is None else q_stride, _addr(cache),
-                                _nbytes(cache), _addr(table), _addr(lens), _addr(out), _addr(lse), _addr(ws),
-                                _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+                                _nbytes(cache), _ints(table, R * per, "table", per), _ints(lens, R, "lens"), _addr(out), _addr(lse),
+                                _addr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
 def norm_desc(rows: int, width: int, u_dtype: int = DT_F32, r_dtype: int = DT_F32, w_dtype: int = DT_F32,

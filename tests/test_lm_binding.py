@@ -1,0 +1,100 @@
+"""What the Python names of include/bitq_lm.h do with tensors that do not hold what the call reads (no GPU needed: every
+refusal comes before the library is called, and what passes ends at its device check)."""
+import pytest
+import torch
+
+import bit_plane_gemv_amd as bq
+
+GPU = torch.cuda.is_available()
+i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+
+
+def buffer(n):
+    """n bytes at a multiple of 256."""
+    b = torch.zeros(n + 256, dtype=torch.uint8)
+    at = -b.data_ptr() % 256
+    return b[at:at + n]
+
+
+def passes(call):
+    """The arguments are taken; there is no device here."""
+    if GPU:
+        pytest.skip("addresses of host memory")
+    with pytest.raises(bq.BitqError) as e:
+        call()
+    assert e.value.status in (bq.E_DEVICE, bq.E_UNSUPPORTED), bq.last_error()
+
+
+KV = bq.kvdesc(2, 64, 16, 10)
+CACHE = buffer(bq.kv_cache_size(KV))
+
+
+def plan(**k):
+    d = bq.kv_plan_desc(3, 16, 4, 10, 20)
+    a = dict(old_len=i32(3), new_len=i32(3), ring=i32(10), state=i32(4), table=i32(3, 4))
+    a.update(k)
+    return lambda: bq.kv_plan(d, *a.values(), buffer(bq.kv_plan_size(d)), stream=0)
+
+
+def write(T=5, **k):
+    a = dict(k=torch.zeros(T, 2, 64), v=torch.zeros(T, 2, 64), x_dtype=bq.DT_F32, slots=i32(T), cache=CACHE)
+    a.update(k)
+    return lambda: bq.kv_write(KV, **a, stream=0)
+
+
+def attn(R=3, **k):
+    d = bq.attn_desc(KV, 4, R, 4, 40, q_dtype=bq.DT_F32, out_dtype=bq.DT_F32)
+    a = dict(q=torch.zeros(R, 4, 64), cache=CACHE, table=i32(R, 4), lens=i32(R), out=torch.zeros(R, 4, 64), ws=None)
+    a.update(k)
+    return lambda: bq.paged_attn(d, **a, stream=0)
+
+
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int16, torch.float32, torch.bool])
+@pytest.mark.parametrize("name", ["old_len", "new_len", "ring", "state", "table"])
+def test_plan_takes_int32_only(name, dtype):
+    with pytest.raises(TypeError, match=name):
+        plan(**{name: torch.zeros(12, dtype=dtype)})()
+
+
+@pytest.mark.parametrize("name,bad", [("old_len", i32(2)), ("new_len", i32(6)[::2]), ("ring", i32(9)), ("state", i32(1)),
+                                      ("table", i32(2, 4)), ("table", i32(4, 3).t()), ("table", i32(3, 5)[:, :4])])
+def test_plan_takes_as_many_as_the_descriptor_says(name, bad):
+    with pytest.raises(ValueError, match=name):
+        plan(**{name: bad})()
+
+
+def test_plan_takes_views_that_hold_them():
+    passes(plan())
+    passes(plan(state=buffer(8), table=i32(12), old_len=i32(8)[2:5]))
+    d = bq.kv_plan_desc(3, 16, 4, 10, 20)
+    passes(plan(old_len=bq.kv_plan_views(d, buffer(bq.kv_plan_size(d)))["len"], table=i32(3, 4)[:, :3]))
+    passes(plan(ring=1 << 20, state=1 << 21))                       # addresses
+
+
+@pytest.mark.parametrize("slots", [torch.zeros(5, dtype=torch.int64), torch.zeros(5)])
+def test_write_takes_int32_slots_only(slots):
+    with pytest.raises(TypeError, match="slots"):
+        write(slots=slots)()
+
+
+def test_write_takes_slots_in_a_row():
+    passes(write())
+    with pytest.raises(ValueError, match="slots"):
+        write(slots=i32(10)[::2])()
+    with pytest.raises(ValueError, match="slots"):
+        write(slots=i32(4), tokens=5)()
+
+
+@pytest.mark.parametrize("name", ["table", "lens"])
+def test_attention_takes_int32_only(name):
+    passes(attn())
+    for dtype in (torch.int64, torch.float32):
+        with pytest.raises(TypeError, match=name):
+            attn(**{name: torch.zeros((3, 4) if name == "table" else 3, dtype=dtype)})()
+
+
+@pytest.mark.parametrize("name,bad", [("lens", i32(2)), ("lens", i32(6)[::2]), ("table", i32(11)), ("table", i32(4, 3).t()),
+                                      ("table", i32(3, 6)[:, :4])])
+def test_attention_takes_as_many_as_the_descriptor_says(name, bad):
+    with pytest.raises(ValueError, match=name):
+        attn(**{name: bad})()
