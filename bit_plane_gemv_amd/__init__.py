@@ -238,6 +238,35 @@ def _ints(x, n: int, name: str, stride: int = 0) -> int | None:
     return x.data_ptr()
 
 
+_FLOATS = {} if _torch is None else {
+    DT_F32: frozenset((_torch.float32, _torch.int32, _torch.uint32)),
+    DT_BF16: frozenset((_torch.bfloat16, _torch.int16, _torch.uint16))}     # (integers: bit patterns)
+
+
+def _float(x, dtype: int, name: str, n: int = 0) -> int | None:
+    """Address of x; a tensor has to have the type the call says (n > 0: and to hold n elements in a row)."""
+    if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if x.dtype not in _FLOATS.get(dtype, (x.dtype,)):
+        raise TypeError(f"{name} is {x.dtype}, the call takes {'bf16' if dtype == DT_BF16 else 'fp32'}")
+    if n and (not x.is_contiguous() or x.numel() < n):
+        raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call writes {n} elements in a row")
+    return x.data_ptr()
+
+
+def _row_stride(x, rows: int, width: int, name: str) -> int:
+    """Elements between the rows of a tensor, `rows` or more, each `width` or more elements next to each other."""
+    shape, st = x.shape, x.stride()
+    size = 1
+    for n, d in zip(shape[:0:-1], st[:0:-1]):
+        if d != size and n != 1:
+            raise ValueError(f"{name}: the elements of a row are not next to each other (shape {tuple(shape)}, strides {st})")
+        size *= n
+    if not st or shape[0] < rows or size < width:
+        raise ValueError(f"{name} has shape {tuple(shape)}, the call reads {rows} rows of {width} elements")
+    return st[0]
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return _raw_stream()
@@ -509,11 +538,14 @@ def kv_plan(desc: KvPlanDesc, old_len, new_len, ring, state, table, plan, stream
 def kv_write(kv: KvDesc, k, v, x_dtype: int, slots, cache, tokens: int | None = None, k_stride: int | None = None,
              v_stride: int | None = None, stream=None):
     """Keys and values of new tokens into their slots (bitq_kv_write).  k, v: tensors [tokens, kv_heads,
-    head_dim] whose last two dimensions are contiguous (or addresses, with the strides given); slots: int32."""
+    head_dim] whose last two dimensions are contiguous (or addresses, with the strides given); slots: int32.  k and v
+    have a row for every slot of the list, the skipped ones too (ValueError otherwise)."""
     tokens = slots.numel() if tokens is None else tokens
-    _check(_lib.bitq_kv_write(kv, _addr(k), _addr(v), x_dtype, k.stride(0) if k_stride is None else k_stride,
-                              v.stride(0) if v_stride is None else v_stride, _ints(slots, tokens, "slots"), tokens, _addr(cache),
-                              _nbytes(cache), _stream(stream)))
+    row = kv.kv_heads * kv.head_dim
+    k_stride = _row_stride(k, tokens, row, "k") if k_stride is None else k_stride
+    v_stride = _row_stride(v, tokens, row, "v") if v_stride is None else v_stride
+    _check(_lib.bitq_kv_write(kv, _float(k, x_dtype, "k"), _float(v, x_dtype, "v"), x_dtype, k_stride, v_stride,
+                              _ints(slots, tokens, "slots"), tokens, _addr(cache), _nbytes(cache), _stream(stream)))
 
 
 def attn_desc(kv: KvDesc, heads: int, requests: int, table_stride: int, max_len: int, window: int = 0,
@@ -528,11 +560,15 @@ def paged_attn_workspace(desc: AttnDesc) -> int:
 
 def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_stride: int | None = None,
                ws_bytes: int | None = None, stream=None):
-    """Attention of one new token per request over the paged cache (bitq_paged_attn).  table and lens: int32."""
-    R, per = desc.requests, desc.table_stride
-    _check(_lib.bitq_paged_attn(desc, _addr(q), q.stride(0) if q_stride is None else q_stride, _addr(cache),
-                                _nbytes(cache), _ints(table, R * per, "table", per), _ints(lens, R, "lens"), _addr(out), _addr(lse),
-                                _addr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+    """Attention of one new token per request over the paged cache (bitq_paged_attn).  q: a tensor [requests, heads,
+    head_dim] whose last two dimensions are contiguous (rows may be longer); out and lse: contiguous; table and lens: int32."""
+    R, per, A = desc.requests, desc.table_stride, desc.requests * desc.heads
+    D = desc.kv.head_dim
+    q_stride = _row_stride(q, R, desc.heads * D, "q") if q_stride is None else q_stride
+    _check(_lib.bitq_paged_attn(desc, _float(q, desc.q_dtype, "q"), q_stride, _addr(cache), _nbytes(cache),
+                                _ints(table, R * per, "table", per), _ints(lens, R, "lens"),
+                                _float(out, desc.out_dtype, "out", A * D), _float(lse, DT_F32, "lse", A), _addr(ws),
+                                _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
 def norm_desc(rows: int, width: int, u_dtype: int = DT_F32, r_dtype: int = DT_F32, w_dtype: int = DT_F32,

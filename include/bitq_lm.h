@@ -119,9 +119,11 @@ bitq_status bitq_kv_plan(const bitq_kv_plan_desc* desc, const int32_t* old_dev, 
  *                 BITQ_DT_BF16), token t starting k_stride (v_stride) elements
  *                 after token t-1 (at least kv_heads * head_dim); naturally
  *                 aligned (rows that are 16-byte aligned are read faster)
- *   slots_dev     i32 [tokens]; slots outside 0 .. pages*page-1 are skipped; a
- *                 slot given twice keeps either token's values, element by
- *                 element
+ *   slots_dev     i32 [tokens]; slots outside 0 .. pages*page-1 are skipped (the
+ *                 rows of their tokens may be read all the same: k_dev and
+ *                 v_dev hold all `tokens` rows); a slot given twice keeps
+ *                 either token's values, element by element (int8: codes and
+ *                 scale may be of different tokens)
  *   cache_dev     the cache, 256-byte aligned
  * bf16 caches round to nearest, ties to even; int8 caches quantize each row.
  * An int8 row with an infinity or NaN gets that as its scale and codes 0: every

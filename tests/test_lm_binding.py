@@ -98,3 +98,54 @@ def test_attention_takes_int32_only(name):
 def test_attention_takes_as_many_as_the_descriptor_says(name, bad):
     with pytest.raises(ValueError, match=name):
         attn(**{name: bad})()
+
+
+f32 = lambda *s: torch.zeros(s)  # noqa: E731
+
+
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("bad,error", [
+    (f32(4, 2, 64), ValueError),                              # fewer rows than slots: they would be read past the end
+    (f32(5, 2, 63), ValueError), (f32(5, 64, 2).transpose(1, 2), ValueError), (f32(5, 2, 128)[..., ::2], ValueError),
+    (f32(2, 5, 64).transpose(0, 1), ValueError),              # heads outermost
+    (f32(5, 2, 64).to(torch.bfloat16), TypeError), (f32(5, 2, 64).double(), TypeError), (f32(5, 2, 64).half(), TypeError),
+])
+def test_write_takes_the_rows_it_reads(name, bad, error):
+    with pytest.raises(error, match=name):
+        write(**{name: bad})()
+
+
+def test_write_reads_a_row_for_every_slot_of_the_list():
+    """A plan's list holds the most tokens of a step, padded with -1: k and v with fewer rows are refused, unless `tokens`
+    says how many slots to take."""
+    p = bq.kv_plan_views(bq.kv_plan_desc(3, 16, 4, 10, 20), buffer(bq.kv_plan_size(bq.kv_plan_desc(3, 16, 4, 10, 20))))
+    with pytest.raises(ValueError, match="k has shape"):
+        write(slots=p["slot"])()
+    passes(write(slots=p["slot"], tokens=5))
+    passes(write(T=20, slots=p["slot"]))
+
+
+def test_write_takes_views_that_hold_the_rows():
+    passes(write(k=f32(5, 4, 64)[:, :2], v=f32(5, 4, 64)[:, 2:]))
+    passes(write(k=f32(5, 128), v=f32(9, 3, 2, 64)[:, 1]))
+    passes(write(k=f32(5, 2, 64).to(torch.bfloat16), v=torch.zeros(5, 2, 64, dtype=torch.int16), x_dtype=bq.DT_BF16))
+    passes(write(k=f32(2000), v=f32(2000), k_stride=130, v_stride=128))
+    passes(write(k=1 << 20, v=1 << 21, k_stride=130, v_stride=128))
+
+
+@pytest.mark.parametrize("name,bad,error", [
+    ("q", f32(2, 4, 64), ValueError), ("q", f32(4, 3, 64).transpose(0, 1), ValueError), ("q", f32(3, 64, 4).transpose(1, 2), ValueError),
+    ("q", f32(3, 4, 63), ValueError), ("q", f32(3, 4, 64).to(torch.bfloat16), TypeError), ("q", f32(3, 4, 64).half(), TypeError),
+    ("out", f32(3, 4, 63), ValueError), ("out", f32(4, 3, 64).transpose(0, 1), ValueError),
+    ("out", torch.zeros(3, 4, 64, dtype=torch.bfloat16), TypeError), ("lse", f32(3, 3), ValueError),
+    ("lse", torch.zeros(3, 4, dtype=torch.bfloat16), TypeError),
+])
+def test_attention_takes_what_the_descriptor_says(name, bad, error):
+    with pytest.raises(error, match=name):
+        attn(**{name: bad})()
+
+
+def test_attention_takes_views_that_hold_the_rows():
+    passes(attn(q=f32(3, 8, 64)[:, :4], out=f32(3, 256), lse=f32(12)))
+    passes(attn(q=f32(3, 300), out=f32(4, 4, 64)))
+    passes(attn(q=1 << 20, q_stride=256, table=1 << 21, lens=1 << 22, out=1 << 23))
