@@ -264,7 +264,7 @@ def _row_stride(x, rows: int, width: int, name: str) -> int:
         size *= n
     if not st or shape[0] < rows or size < width:
         raise ValueError(f"{name} has shape {tuple(shape)}, the call reads {rows} rows of {width} elements")
-    return st[0]
+    return st[0] if shape[0] > 1 else size      # (the stride of a single row means nothing)
 
 
 def _stream(stream) -> int | None:

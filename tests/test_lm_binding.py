@@ -149,3 +149,13 @@ def test_attention_takes_views_that_hold_the_rows():
     passes(attn(q=f32(3, 8, 64)[:, :4], out=f32(3, 256), lse=f32(12)))
     passes(attn(q=f32(3, 300), out=f32(4, 4, 64)))
     passes(attn(q=1 << 20, q_stride=256, table=1 << 21, lens=1 << 22, out=1 << 23))
+
+
+def test_a_single_row_has_any_stride():
+    """The stride of a dimension of size 1 is arbitrary: a transposed or expanded single row is still one row."""
+    one = f32(2, 1, 64).transpose(0, 1)
+    assert one.stride(0) == 64
+    passes(write(T=1, k=one, v=one))
+    passes(write(T=1, k=f32(2, 64).expand(1, 2, 64)))
+    d = bq.attn_desc(KV, 4, 1, 4, 40, q_dtype=bq.DT_F32, out_dtype=bq.DT_F32)
+    passes(lambda: bq.paged_attn(d, f32(4, 1, 64).transpose(0, 1), CACHE, i32(1, 4), i32(1), f32(1, 4, 64), None, stream=0))
