@@ -218,45 +218,52 @@ def _addr(x) -> int | None:
         return _ptr(x)
 
 
-# Element types of a tensor of int32 values: what else holds them would be read as something else.
-_WORDS = frozenset() if _torch is None else frozenset((_torch.int32, _torch.uint32, _torch.uint8))
+# What the calls of a decode step read is checked here, the ordinary tensor first (a check costs the host 0.1 to 0.3 us).
+if _torch is not None:
+    _I32, _WORDS = _torch.int32, frozenset((_torch.int32, _torch.uint32, _torch.uint8))
+    _FLOATS = {DT_F32: frozenset((_torch.float32, _torch.int32, _torch.uint32)),             # (integers: bit patterns)
+               DT_BF16: frozenset((_torch.bfloat16, _torch.int16, _torch.uint16))}
 
 
 def _ints(x, n: int, name: str, stride: int = 0) -> int | None:
     """Address of n int32 values in a row; a tensor has to hold them (a table: in rows `stride` apart)."""
-    if x is None or isinstance(x, int):
-        return x
-    if not hasattr(x, "data_ptr"):
+    try:
+        if x.dtype is _I32 and x.is_contiguous() and x.nbytes >= 4 * n:
+            return x.data_ptr()
+        at = x.data_ptr()
+    except AttributeError:                       # (no tensor)
         return _ptr(x)
     if x.dtype not in _WORDS:
         raise TypeError(f"{name} must be int32, not {x.dtype}")
     if not x.is_contiguous():
         if not stride or x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != stride or x.size(0) * stride < n:
             raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call reads {n} values in a row")
-    elif x.numel() * x.element_size() < 4 * n:
+    elif x.nbytes < 4 * n:
         raise ValueError(f"{name} has {x.numel()} values, the call needs {n}")
-    return x.data_ptr()
-
-
-_FLOATS = {} if _torch is None else {
-    DT_F32: frozenset((_torch.float32, _torch.int32, _torch.uint32)),
-    DT_BF16: frozenset((_torch.bfloat16, _torch.int16, _torch.uint16))}     # (integers: bit patterns)
+    return at
 
 
 def _float(x, dtype: int, name: str, n: int = 0) -> int | None:
     """Address of x; a tensor has to have the type the call says (n > 0: and to hold n elements in a row)."""
-    if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
+    try:
+        at = x.data_ptr()
+    except AttributeError:                       # (no tensor)
         return _ptr(x)
-    if x.dtype not in _FLOATS.get(dtype, (x.dtype,)):
+    if dtype in _FLOATS and x.dtype not in _FLOATS[dtype]:
         raise TypeError(f"{name} is {x.dtype}, the call takes {'bf16' if dtype == DT_BF16 else 'fp32'}")
-    if n and (not x.is_contiguous() or x.numel() < n):
+    if n and not (x.is_contiguous() and x.numel() >= n):
         raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call writes {n} elements in a row")
-    return x.data_ptr()
+    return at
 
 
 def _row_stride(x, rows: int, width: int, name: str) -> int:
     """Elements between the rows of a tensor, `rows` or more, each `width` or more elements next to each other."""
     shape, st = x.shape, x.stride()
+    if len(st) == 3:
+        n, h, d = shape
+        a, b, c = st
+        if c == 1 and b == d and n >= rows and n > 1 and h * d >= width:
+            return a
     size = 1
     for n, d in zip(shape[:0:-1], st[:0:-1]):
         if d != size and n != 1:
@@ -457,7 +464,7 @@ def quantize_act_hgf_noalloc(desc: WDesc, w, x, x_dtype: int, M: int, act, act_b
 
 def _nbytes(buf) -> int:
     """Size of a device buffer (0 for None: calls that need no workspace)."""
-    return 0 if buf is None else buf.numel() * buf.element_size()
+    return 0 if buf is None else buf.nbytes
 
 
 def gemv(desc: WDesc, w, x, x_dtype: int, y, ws, ws_bytes: int | None = None, flags: int = 0,
