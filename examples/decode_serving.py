@@ -1,12 +1,13 @@
 """A small decoder served with packed layers, a paged cache and an int8 head.
 
-    python examples/decode_serving.py [--requests 6] [--steps 40]
+    python examples/decode_serving.py [--requests 6] [--steps 40] [--pages 13]
 
 Random weights of a toy shape.  Each step every active request feeds one token: the plan gives it a slot in the paged
 cache, the blocks' linear layers run on 2-bit weights with int8 activations (bitq_gemm_smallM), keys and values go to
 the cache, attention reads the pages, the residual stream passes the norms before and after each block, and the head is
 an int8 product on the rows that the last norm quantized.  Requests begin and end at different steps; their pages go
-back to the ring and are used again.
+back to the ring and are used again.  A request that the plan refuses for want of pages asks again with the same token,
+and the last request of the batch gives its pages up and begins anew.
 """
 from __future__ import annotations
 
@@ -43,9 +44,10 @@ class Packed:
 
 
 class Server:
-    """`requests` slots (2 to 64), each holding one request at a time."""
+    """`requests` slots (2 to 64), each holding one request at a time; `pages` pages of the cache for all of them (at least
+    those of one request)."""
 
-    def __init__(self, requests, seed=0):
+    def __init__(self, requests, seed=0, pages=None):
         rng = np.random.default_rng(seed)
         R = self.R = requests
         f = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()  # noqa: E731
@@ -61,7 +63,8 @@ class Server:
                       self.head_scale)
         # the cache: one pool of pages per layer, one table and one ring for all layers
         self.stride = MAX_LEN // PAGE
-        self.pages = R * self.stride // 2 + 1                 # fewer than every request at full length would need
+        # (by default half of what every request at full length would need, which is what serve() asks for at most)
+        self.pages = R * self.stride // 2 + 1 if pages is None else pages
         self.kv = bq.kvdesc(KV_HEADS, DIM, PAGE, self.pages)
         self.caches = [torch.empty(bq.kv_cache_size(self.kv), dtype=torch.uint8, device="cuda") for _ in range(LAYERS)]
         self.table = torch.full((R, self.stride), -1, dtype=torch.int32, device="cuda")
@@ -111,25 +114,41 @@ class Server:
         return self.logits, now["len"]
 
 
-def serve(requests, steps, seed=0, follow=None):
+def serve(requests, steps, seed=0, follow=None, pages=None):
     """Requests of random lengths on `requests` slots, each continuing with its own most likely token.  follow(server,
-    tokens, active, logits, lengths) is called after each step.  Returns the number of tokens served and of requests ended."""
-    server = Server(requests, seed)
+    tokens, active, logits, lengths) is called after each step.  Returns the number of tokens served (written to the cache
+    and attended) and of requests ended."""
+    server = Server(requests, seed, pages)
     rng = np.random.default_rng(seed + 1)
-    left = rng.integers(1, MAX_LEN // 2, requests)
-    tokens = torch.from_numpy(rng.integers(0, VOCAB, requests).astype(np.int32)).cuda()
+    total = rng.integers(1, MAX_LEN // 2, requests)           # tokens of each slot's request, its first one,
+    first = torch.from_numpy(rng.integers(0, VOCAB, requests).astype(np.int32)).cuda()
+    left, tokens = total.copy(), first                        # those to come and the next one
+    held, yields = np.zeros(requests, int), np.zeros(requests, bool)
     served = ended = 0
     for _ in range(steps):
-        active = (left > 0).astype(np.int32)
+        active = (left > 0) & ~yields
+        act = torch.from_numpy(active.astype(np.int32)).cuda()
         fresh = torch.from_numpy(rng.integers(0, VOCAB, requests).astype(np.int32)).cuda()
-        act = torch.from_numpy(active).cuda()
         logits, lengths = server.step(tokens, act)
         if follow:
             follow(server, tokens, act, logits, lengths)
-        tokens = torch.where(act > 0, logits.argmax(1).to(torch.int32), fresh)
-        served += int(active.sum())
-        ended += int((active == 0).sum())
-        left = np.where(active > 0, left - 1, rng.integers(1, MAX_LEN // 2, requests))   # an ended slot takes a new request
+        now = lengths.cpu().numpy()
+        written = active & (now > held)                       # the other active ones were refused
+        served += int(written.sum())
+        done = ~active & ~yields                              # an ended slot takes a new request
+        ended += int(done.sum())
+        total = np.where(done, rng.integers(1, MAX_LEN // 2, requests), total)
+        left = np.where(written, left - 1, np.where(active, left, total))
+        dev = lambda m: torch.from_numpy(m).cuda()  # noqa: E731
+        first = torch.where(dev(done), fresh, first)
+        tokens = torch.where(dev(written), logits.argmax(1).to(torch.int32), torch.where(dev(active), tokens, first))
+        # the plan serves requests in order and stops at the first that does not fit: unless a request ends by itself, the
+        # last one makes room, so the first one always goes on
+        yields = np.zeros(requests, bool)
+        going = np.flatnonzero(active & (left > 0))
+        if (active & ~written).any() and len(going) == active.sum() > 1:
+            yields[going[-1]] = True
+        held = now
     return served, ended
 
 
@@ -137,7 +156,9 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--requests", type=int, default=6)
     ap.add_argument("--steps", type=int, default=40)
+    ap.add_argument("--pages", type=int, help="pages of each layer's cache")
     a = ap.parse_args()
-    served, ended = serve(a.requests, a.steps)
+    served, ended = serve(a.requests, a.steps, pages=a.pages)
     torch.cuda.synchronize()
-    print(f"{served} tokens served, {ended} requests ended, {a.requests} slots, {Server(a.requests).pages} pages per layer")
+    pages = Server(a.requests, pages=a.pages).pages
+    print(f"{served} tokens served, {ended} requests ended, {a.requests} slots, {pages} pages per layer")
