@@ -39,6 +39,7 @@ from __future__ import annotations
 
 import argparse
 import hashlib
+import importlib.util
 import json
 import math
 import os
@@ -63,14 +64,14 @@ METRIC = "packed-weight GB/s & % HBM peak, bit-plane GEMV 11008x4096 M=1; us/lay
 # HBM bytes moved per launch of a product kernel, from rocprofv3 counter runs
 # (FETCH_SIZE x 2.0 + WRITE_SIZE x 1.0; factors calibrated on a plain copy
 # kernel of known size; profiles/ holds the runs).  Each entry is valid only
-# for the kernel source and the build script it was measured with (first 16
-# hex digits of the sha256 of each file); otherwise traffic is reported as null.
+# for the kernel source and the compiler flags it was measured with (first 16
+# hex digits of their sha256); otherwise traffic is reported as null.
 MEASURED_TRAFFIC: dict = {
-    "rabit": {"source": "bitq_sign.hip", "sha16": "ba906aeaa6be2c6a", "build_sha16": "75709457503c2a5c",
+    "rabit": {"source": "bitq_sign.hip", "sha16": "ba906aeaa6be2c6a", "flags_sha16": "697bc7a40f55c58f",
               "bytes_per_launch": 13458432, "profile": "profiles/gemv_sign_kernel_rabit_11008x4096.md"},
-    "w2a8": {"source": "bitq_bits.hip", "sha16": "241574416dea4db5", "build_sha16": "75709457503c2a5c",
+    "w2a8": {"source": "bitq_bits.hip", "sha16": "241574416dea4db5", "flags_sha16": "697bc7a40f55c58f",
              "bytes_per_launch": 12822528, "profile": "profiles/gemv_bits_nr_kernel_w2a8_11008x4096.md"},
-    "w2a8+fuse": {"source": "bitq_bits.hip", "sha16": "241574416dea4db5", "build_sha16": "75709457503c2a5c",
+    "w2a8+fuse": {"source": "bitq_bits.hip", "sha16": "241574416dea4db5", "flags_sha16": "697bc7a40f55c58f",
                   "bytes_per_launch": 12880896, "profile": "profiles/gemv_bits_nr_kernel_fused_w2a8_11008x4096.md"},
 }
 BUILD_SCRIPT = os.path.join(ROOT, "bit_plane_gemv_amd", "build.py")
@@ -81,14 +82,18 @@ def source_sha(name: str) -> str:
         return hashlib.sha256(f.read()).hexdigest()[:16]
 
 
-def build_sha() -> str:
-    with open(BUILD_SCRIPT, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+def flags_sha(script: str = BUILD_SCRIPT) -> str:
+    """Of the flags that the kernels are compiled with (the include path, which names where the tree lies, left out)."""
+    spec = importlib.util.spec_from_file_location("bitq_build", script)
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    flags = [f for f in [*build.COMMON, *build.DEVICE_FLAGS] if not f.startswith("-I")]
+    return hashlib.sha256("\n".join(flags).encode()).hexdigest()[:16]
 
 
 def measured_traffic(key: str):
     mt = MEASURED_TRAFFIC.get(key)
-    if mt is None or mt["sha16"] != source_sha(mt["source"]) or mt["build_sha16"] != build_sha():
+    if mt is None or mt["sha16"] != source_sha(mt["source"]) or mt["flags_sha16"] != flags_sha():
         return None
     return mt
 
