@@ -314,10 +314,14 @@ __device__ __forceinline__ float row_codes(float (&v)[8], int LR) {
     const float a = __uint_as_float(m);
     const float s = a > 0.0f ? __fdiv_rn(127.0f, a) : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float q = rintf(__fmul_rn(v[e], s));
-        v[e] = q == q ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], s);
+    if (!(a < INFINITY && s < INFINITY)) {  // (a branch that rows of ordinary numbers skip: 8 selects fewer)
+        asm volatile("");
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] == v[e] ? v[e] : 0.0f;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(rintf(v[e]), -127.0f), 127.0f);
     return __fdiv_rn(a, 127.0f);
 }
 

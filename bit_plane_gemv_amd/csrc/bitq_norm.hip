@@ -299,11 +299,20 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(NormA
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // (NaN: an infinity or NaN in the row, whose scale says so, or a zero where 127 / m overflows)
-                    const float q = rintf(__fmul_rn(y[j][e], f));
-                    y[j][e] = q == q ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
-                }
+                for (int e = 0; e < 8; ++e) y[j][e] = __fmul_rn(y[j][e], f);
+            if (!(m < INFINITY && f < INFINITY)) {
+                // NaN: an infinity or NaN in the row, whose scale says so, or
+                // a zero where 127 / m overflows (a branch, which other rows skip)
+                asm volatile("");
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[j][e] = y[j][e] == y[j][e] ? y[j][e] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[j][e] = fminf(fmaxf(rintf(y[j][e]), -127.0f), 127.0f);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
