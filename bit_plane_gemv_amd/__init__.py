@@ -256,14 +256,17 @@ def _float(x, dtype: int, name: str, n: int = 0) -> int | None:
     return at
 
 
-def _row_stride(x, rows: int, width: int, name: str) -> int:
-    """Elements between the rows of a tensor, `rows` or more, each `width` or more elements next to each other."""
+def _rows(x, rows: int, width: int, dtype: int, name: str, stride: int | None) -> tuple:
+    """Address of x and the elements between its rows: `rows` or more, each `width` or more elements of the call's type
+    next to each other.  An address comes with its stride, which is believed."""
+    if stride is not None:
+        return _float(x, dtype, name), stride
     shape, st = x.shape, x.stride()
     if len(st) == 3:
         n, h, d = shape
         a, b, c = st
-        if c == 1 and b == d and n >= rows and n > 1 and h * d >= width:
-            return a
+        if c == 1 and b == d and n >= rows and n > 1 and h * d >= width and x.dtype in _FLOATS.get(dtype, ()):
+            return x.data_ptr(), a
     size = 1
     for n, d in zip(shape[:0:-1], st[:0:-1]):
         if d != size and n != 1:
@@ -271,7 +274,7 @@ def _row_stride(x, rows: int, width: int, name: str) -> int:
         size *= n
     if not st or shape[0] < rows or size < width:
         raise ValueError(f"{name} has shape {tuple(shape)}, the call reads {rows} rows of {width} elements")
-    return st[0] if shape[0] > 1 else size      # (the stride of a single row means nothing)
+    return _float(x, dtype, name), st[0] if shape[0] > 1 else size      # (the stride of a single row means nothing)
 
 
 def _stream(stream) -> int | None:
@@ -549,10 +552,10 @@ def kv_write(kv: KvDesc, k, v, x_dtype: int, slots, cache, tokens: int | None = 
     have a row for every slot of the list, the skipped ones too (ValueError otherwise)."""
     tokens = slots.numel() if tokens is None else tokens
     row = kv.kv_heads * kv.head_dim
-    k_stride = _row_stride(k, tokens, row, "k") if k_stride is None else k_stride
-    v_stride = _row_stride(v, tokens, row, "v") if v_stride is None else v_stride
-    _check(_lib.bitq_kv_write(kv, _float(k, x_dtype, "k"), _float(v, x_dtype, "v"), x_dtype, k_stride, v_stride,
-                              _ints(slots, tokens, "slots"), tokens, _addr(cache), _nbytes(cache), _stream(stream)))
+    k_at, k_stride = _rows(k, tokens, row, x_dtype, "k", k_stride)
+    v_at, v_stride = _rows(v, tokens, row, x_dtype, "v", v_stride)
+    _check(_lib.bitq_kv_write(kv, k_at, v_at, x_dtype, k_stride, v_stride, _ints(slots, tokens, "slots"), tokens, _addr(cache),
+                              _nbytes(cache), _stream(stream)))
 
 
 def attn_desc(kv: KvDesc, heads: int, requests: int, table_stride: int, max_len: int, window: int = 0,
@@ -571,8 +574,8 @@ def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_strid
     head_dim] whose last two dimensions are contiguous (rows may be longer); out and lse: contiguous; table and lens: int32."""
     R, per, A = desc.requests, desc.table_stride, desc.requests * desc.heads
     D = desc.kv.head_dim
-    q_stride = _row_stride(q, R, desc.heads * D, "q") if q_stride is None else q_stride
-    _check(_lib.bitq_paged_attn(desc, _float(q, desc.q_dtype, "q"), q_stride, _addr(cache), _nbytes(cache),
+    q_at, q_stride = _rows(q, R, desc.heads * D, desc.q_dtype, "q", q_stride)
+    _check(_lib.bitq_paged_attn(desc, q_at, q_stride, _addr(cache), _nbytes(cache),
                                 _ints(table, R * per, "table", per), _ints(lens, R, "lens"),
                                 _float(out, desc.out_dtype, "out", A * D), _float(lse, DT_F32, "lse", A), _addr(ws),
                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
