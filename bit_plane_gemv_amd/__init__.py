@@ -220,7 +220,7 @@ def _addr(x) -> int | None:
 
 # What the calls of a decode step read is checked here, the ordinary tensor first (a check costs the host 0.1 to 0.3 us).
 if _torch is not None:
-    _I32, _WORDS = _torch.int32, frozenset((_torch.int32, _torch.uint32, _torch.uint8))
+    _INT, _WORDS = _torch.int32, frozenset((_torch.int32, _torch.uint32, _torch.uint8))
     _FLOATS = {DT_F32: frozenset((_torch.float32, _torch.int32, _torch.uint32)),             # (integers: bit patterns)
                DT_BF16: frozenset((_torch.bfloat16, _torch.int16, _torch.uint16))}
 
@@ -228,7 +228,7 @@ if _torch is not None:
 def _ints(x, n: int, name: str, stride: int = 0) -> int | None:
     """Address of n int32 values in a row; a tensor has to hold them (a table: in rows `stride` apart)."""
     try:
-        if x.dtype is _I32 and x.is_contiguous() and x.nbytes >= 4 * n:
+        if x.dtype is _INT and x.is_contiguous() and x.nbytes >= 4 * n:
             return x.data_ptr()
         at = x.data_ptr()
     except AttributeError:                       # (no tensor)

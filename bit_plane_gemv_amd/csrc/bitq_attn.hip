@@ -31,10 +31,10 @@ namespace bitq {
 // scores are those of 8 consecutive tokens 8 g .. 8 g + 7 of head j: exactly
 // the B operand that the second product needs from that lane, with no
 // movement between lanes.  V's layout (8 tokens of an element together) makes
-// its A operand one 16-byte load.  All operands go from memory to registers;
-// LDS is used only to join the waves at the end.  With fewer than 16 query
-// heads per key-value head columns idle: the matrix cores need a tenth of the
-// memory's time even so.
+// its A operand one 16-byte load.  Keys and values go from memory to registers;
+// LDS holds the queries' operands and joins the waves at the end.  With fewer
+// than 16 query heads per key-value head columns idle: the matrix cores need a
+// tenth of the memory's time even so.
 //
 // Precision.  bf16 and int8 cache rows are exact in bf16; int8 scales are
 // applied in fp32, to the scores and to p.  fp32 q is split into 3 bf16

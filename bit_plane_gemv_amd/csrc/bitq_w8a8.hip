@@ -167,7 +167,9 @@ __global__ __launch_bounds__(64 * KW) void w8a8_few_kernel(GemmArgs g) {
 // cores and LDS, which a 256 x 256 tile loads alike (1024 cycles of products,
 // 768 of operand reads and 256 of copies per unit), at the clock that their
 // power allows: 4096 x 8192 x 8192 231 us, 2.38 POP/s, what a library product
-// of 8192^3 reaches; 4096 x 11008 x 4096 164 - 180 us, 2.05 - 2.25 POP/s, its
+// of 8192^3 reaches; 4096 x 11008 x 4096 170 us in a run of 1500 calls, 177 a
+// call with pauses of 10 ms, 190 - 200 in the first 20 calls after a pause (a
+// library's product without scales: 179, 203 and 203 - 209 there), its
 // 688 tiles filling 2.7 of 3 rounds.  (Waves of 128 x 128, with fewer operand
 // reads, but one to a SIMD: 198 us.)  Few tokens: bound by the weight stream
 // and the ramp of its few workgroups (64 x 4096 x 11008: 10 us and the join's 4).
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(GemmArgs g, int tiles_m,
 // Tiles: 64 x 64, 64 x 128, 128 x 128, 256 x 256 with k ranges of 4096 take
 // about max(11, 8.5 x), 14 ceil(x), max(18, 24 x) and (x <= 1: 40 + 17 x,
 // else 57 ceil(x)) us for x = tiles / 256; the smallest is taken.
-// (4096 x 11008 x 4096: 256 x 256 164 us, 128 x 128 227; 1024 x 4096 x 4096:
+// (Short runs: 4096 x 11008 x 4096: 256 x 256 164 us, 128 x 128 227; 1024 x 4096 x 4096:
 // 128 x 128 22.0, 256 x 256 40.6, 64 x 128 27.5; 512: 64 x 128 14.6, 64 x 64
 // 16.4, 128 x 128 19.1; 256: 64 x 64 11.6, 64 x 128 13.5.)
 // Too few 64 x 64 tiles for the CUs and a long k: the k range is split and

@@ -159,3 +159,9 @@ def test_a_single_row_has_any_stride():
     passes(write(T=1, k=f32(2, 64).expand(1, 2, 64)))
     d = bq.attn_desc(KV, 4, 1, 4, 40, q_dtype=bq.DT_F32, out_dtype=bq.DT_F32)
     passes(lambda: bq.paged_attn(d, f32(4, 1, 64).transpose(0, 1), CACHE, i32(1, 4), i32(1), f32(1, 4, 64), None, stream=0))
+
+
+def test_names_of_the_older_calls_are_untouched():
+    """The binding's own abbreviations do not hide each other (a launch shape needs ctypes integers)."""
+    grid, block = bq.ctx_launch_shape(bq.wdesc("rabit", 11008, 4096), 1, bq.DT_BF16, 0)
+    assert grid > 0 and block > 0
