@@ -53,6 +53,8 @@ SIGN1, RABIT, TERNARY, W2A8, BVSR4, WNAM, HGF = 1, 2, 3, 4, 5, 6, 7
 DT_F32, DT_BF16, DT_ACT, DT_BINARY = 0, 1, 2, 3
 DT_ROW8 = 16       # bitq_block_norm: int8 rows with a scale each
 KV_BF16, KV_INT8 = 0, 1
+ROPE_HALF, ROPE_PAIRS = 0, 1                                     # the order of a rotated pair's elements
+ROPE_PLAIN, ROPE_LINEAR, ROPE_RAMP, ROPE_BAND = 0, 1, 2, 3       # how frequencies are stretched
 F_ACC_INT32 = 1
 F_FUSE_QUANT = 2   # bitq_gemv: raw x, the activation quantizer runs in the GEMV kernel
 
@@ -119,6 +121,34 @@ class W8A8Desc(ctypes.Structure):
                 ("lda", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("flags", ctypes.c_uint32)]
 
 
+class PromptDesc(ctypes.Structure):
+    _fields_ = [("kv", KvDesc), ("heads", ctypes.c_int32), ("requests", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("max_len", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("q_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class SharedDesc(ctypes.Structure):
+    _fields_ = [("attn", AttnDesc), ("groups", ctypes.c_int32), ("max_prefix", ctypes.c_int32)]
+
+
+class KvPagesDesc(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int32), ("page", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("pool", ctypes.c_int32), ("moves", ctypes.c_int32)]
+
+
+class RopeFreq(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("trained", ctypes.c_double), ("turns_keep", ctypes.c_double), ("turns_scale", ctypes.c_double)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("mscale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -151,6 +181,17 @@ _sigs = {
     "bitq_kv_write": ([ctypes.POINTER(KvDesc), _P, _P, _I32, _I64, _I64, _P, _I32, _P, _SZ, _P], _I32),
     "bitq_paged_attn_workspace": ([ctypes.POINTER(AttnDesc), ctypes.POINTER(_SZ)], _I32),
     "bitq_paged_attn": ([ctypes.POINTER(AttnDesc), _P, _I64, _P, _SZ, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "bitq_prompt_attn_workspace": ([ctypes.POINTER(PromptDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_prompt_attn": ([ctypes.POINTER(PromptDesc), _P, _I64, _P, _SZ, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "bitq_shared_attn_workspace": ([ctypes.POINTER(SharedDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_shared_attn": ([ctypes.POINTER(SharedDesc), _P, _I64, _P, _SZ, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "bitq_kv_pages_size": ([ctypes.POINTER(KvPagesDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_kv_pages_workspace": ([ctypes.POINTER(KvPagesDesc), ctypes.POINTER(_SZ)], _I32),
+    "bitq_kv_fork": ([ctypes.POINTER(KvPagesDesc), _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _SZ, _P], _I32),
+    "bitq_kv_compact": ([ctypes.POINTER(KvPagesDesc), _P, _P, _P, _P, _P, _SZ, _P, _SZ, _P], _I32),
+    "bitq_kv_copy": ([ctypes.POINTER(KvDesc), _P, _P, _I32, _P, _SZ, _P], _I32),
+    "bitq_rope_table": ([ctypes.POINTER(RopeFreq), _P], _I32),
+    "bitq_qk_rope": ([ctypes.POINTER(RopeDesc), _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _P], _I32),
     "bitq_block_norm": ([ctypes.POINTER(NormDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
     "bitq_w8a8_workspace": ([ctypes.POINTER(W8A8Desc), ctypes.POINTER(_SZ)], _I32),
     "bitq_gemm_w8a8": ([ctypes.POINTER(W8A8Desc), _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
@@ -240,6 +281,19 @@ def _ints(x, n: int, name: str, stride: int = 0) -> int | None:
             raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call reads {n} values in a row")
     elif x.nbytes < 4 * n:
         raise ValueError(f"{name} has {x.numel()} values, the call needs {n}")
+    return at
+
+
+def _longs(x, n: int, name: str) -> int | None:
+    """Address of n 64-bit integers in a row."""
+    try:
+        at = x.data_ptr()
+    except AttributeError:                       # (no tensor)
+        return _ptr(x)
+    if x.dtype not in (_torch.int64, _torch.uint64):
+        raise TypeError(f"{name} must be int64 or uint64, not {x.dtype}")
+    if not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{name} has shape {tuple(x.shape)} and strides {x.stride()}, the call reads {n} values in a row")
     return at
 
 
@@ -579,6 +633,131 @@ def paged_attn(desc: AttnDesc, q, cache, table, lens, out, ws, lse=None, q_strid
                                 _ints(table, R * per, "table", per), _ints(lens, R, "lens"),
                                 _float(out, desc.out_dtype, "out", A * D), _float(lse, DT_F32, "lse", A), _addr(ws),
                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def prompt_desc(kv: KvDesc, heads: int, requests: int, tokens: int, table_stride: int, max_len: int, window: int = 0,
+                sinks: int = 0, q_dtype: int = DT_BF16, out_dtype: int = DT_BF16, scale: float | None = None) -> PromptDesc:
+    return PromptDesc(kv, heads, requests, tokens, table_stride, max_len, window, sinks, q_dtype, out_dtype,
+                      kv.head_dim ** -0.5 if scale is None else scale)
+
+
+def prompt_attn_workspace(desc: PromptDesc) -> int:
+    return _size_of(_lib.bitq_prompt_attn_workspace, desc)
+
+
+def prompt_attn(desc: PromptDesc, q, cache, table, start, lens, out, ws, lse=None, q_stride: int | None = None,
+                ws_bytes: int | None = None, stream=None):
+    """Attention of each request's new tokens, rows start[r] .. start[r + 1] - 1 of q, over the paged cache that holds them
+    already (bitq_prompt_attn).  q: a tensor [tokens, heads, head_dim] whose last two dimensions are contiguous (rows may be
+    longer); out and lse: contiguous; table, start and lens: int32."""
+    R, per, A = desc.requests, desc.table_stride, desc.tokens * desc.heads
+    D = desc.kv.head_dim
+    q_at, q_stride = _rows(q, desc.tokens, desc.heads * D, desc.q_dtype, "q", q_stride)
+    _check(_lib.bitq_prompt_attn(desc, q_at, q_stride, _addr(cache), _nbytes(cache), _ints(table, R * per, "table", per),
+                                 _ints(start, R + 1, "start"), _ints(lens, R, "lens"),
+                                 _float(out, desc.out_dtype, "out", A * D), _float(lse, DT_F32, "lse", A), _addr(ws),
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def shared_desc(attn: AttnDesc, groups: int, max_prefix: int) -> SharedDesc:
+    return SharedDesc(attn, groups, max_prefix)
+
+
+def shared_attn_workspace(desc: SharedDesc) -> int:
+    return _size_of(_lib.bitq_shared_attn_workspace, desc)
+
+
+def shared_attn(desc: SharedDesc, q, cache, table, lens, start, prefix, out, ws, lse=None, q_stride: int | None = None,
+                ws_bytes: int | None = None, stream=None):
+    """paged_attn for groups of requests, start[g] .. start[g + 1] - 1, that have their first prefix[g] tokens in common:
+    those are read once for the group (bitq_shared_attn).  Tensors as for paged_attn; start and prefix: int32."""
+    a = desc.attn
+    R, per, A = a.requests, a.table_stride, a.requests * a.heads
+    D = a.kv.head_dim
+    q_at, q_stride = _rows(q, R, a.heads * D, a.q_dtype, "q", q_stride)
+    _check(_lib.bitq_shared_attn(desc, q_at, q_stride, _addr(cache), _nbytes(cache), _ints(table, R * per, "table", per),
+                                 _ints(lens, R, "lens"), _ints(start, desc.groups + 1, "start"),
+                                 _ints(prefix, desc.groups, "prefix"), _float(out, a.out_dtype, "out", A * D),
+                                 _float(lse, DT_F32, "lse", A), _addr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                 _stream(stream)))
+
+
+def kv_pages_desc(requests: int, page: int, table_stride: int, pool: int, moves: int) -> KvPagesDesc:
+    return KvPagesDesc(requests, page, table_stride, pool, moves)
+
+
+def kv_pages_size(desc: KvPagesDesc) -> int:
+    return _size_of(_lib.bitq_kv_pages_size, desc)
+
+
+def kv_pages_workspace(desc: KvPagesDesc) -> int:
+    return _size_of(_lib.bitq_kv_pages_workspace, desc)
+
+
+def kv_pages_views(desc: KvPagesDesc, result) -> dict:
+    """Sections of the result buffer (a uint8 tensor) of kv_fork and kv_compact as int32 tensors: state, len, frm, to."""
+    import torch
+    out, at = {}, 0
+    for name, n in (("state", 4), ("len", desc.requests), ("frm", desc.moves), ("to", desc.moves)):
+        out[name] = result[at:at + 4 * n].view(torch.int32)
+        at += (4 * n + 255) // 256 * 256
+    return out
+
+
+def kv_fork(desc: KvPagesDesc, src, keep, lens, ring, state, table, table_out, result, ws, stream=None):
+    """Request r becomes the first keep[r] tokens of request src[r]: forks, cuts, ends (bitq_kv_fork).  All int32; the
+    copies of pages that result's frm and to list are the caller's to make, in every layer's cache (kv_copy)."""
+    R, per = desc.requests, desc.table_stride
+    _check(_lib.bitq_kv_fork(desc, _ints(src, R, "src"), _ints(keep, R, "keep"), _ints(lens, R, "lens"),
+                             _ints(ring, desc.pool, "ring"), _ints(state, 2, "state"), _ints(table, R * per, "table", per),
+                             _ints(table_out, R * per, "table_out", per), _addr(result), _nbytes(result), _addr(ws),
+                             _nbytes(ws), _stream(stream)))
+
+
+def kv_compact(desc: KvPagesDesc, lens, table, table_out, ring, result, ws, stream=None):
+    """Held pages to the low end of the pool (bitq_kv_compact): tables, ring and the list of copies as for kv_fork."""
+    R, per = desc.requests, desc.table_stride
+    _check(_lib.bitq_kv_compact(desc, _ints(lens, R, "lens"), _ints(table, R * per, "table", per),
+                                _ints(table_out, R * per, "table_out", per), _ints(ring, desc.pool, "ring"), _addr(result),
+                                _nbytes(result), _addr(ws), _nbytes(ws), _stream(stream)))
+
+
+def kv_copy(kv: KvDesc, frm, to, cache, moves: int | None = None, stream=None):
+    """Pages frm[i] of a layer's cache to pages to[i] (bitq_kv_copy); pairs with an index outside the pool are skipped."""
+    moves = to.numel() if moves is None else moves
+    _check(_lib.bitq_kv_copy(kv, _ints(frm, moves, "frm"), _ints(to, moves, "to"), moves, _addr(cache), _nbytes(cache),
+                             _stream(stream)))
+
+
+def rope_table(rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0, trained: float = 0.0,
+               turns_keep: float = 0.0, turns_scale: float = 0.0) -> np.ndarray:
+    """The rotation's turns per position as 64-bit fractions, uint64 [rot / 2] (bitq_rope_table); for qk_rope on the GPU:
+    torch.from_numpy(table).cuda()."""
+    out = np.empty(max(1, rot // 2), dtype=np.uint64)
+    _check(_lib.bitq_rope_table(RopeFreq(rot, kind, base, factor, trained, turns_keep, turns_scale), out.ctypes.data))
+    return out
+
+
+def rope_desc(tokens: int, q_heads: int, k_heads: int, head_dim: int, rot: int | None = None, layout: int = ROPE_HALF,
+              x_dtype: int = DT_F32, out_dtype: int = DT_BF16, w_dtype: int = DT_F32, eps: float = 1e-6,
+              mscale: float = 1.0) -> RopeDesc:
+    return RopeDesc(tokens, q_heads, k_heads, head_dim, head_dim if rot is None else rot, layout, x_dtype, out_dtype,
+                    w_dtype, eps, mscale)
+
+
+def qk_rope(desc: RopeDesc, q, k, q_w, k_w, table, pos, q_out, k_out, strides: tuple = (None,) * 4, stream=None):
+    """Norms of queries and keys head by head, and their rotation (bitq_qk_rope).  q, k and the outputs: tensors [tokens,
+    heads, head_dim] whose last two dimensions are contiguous (or addresses, with the four strides given), None without heads;
+    q_w, k_w: [head_dim] or None; table: rope_table's values on the GPU; pos: int32."""
+    T, D = desc.tokens, desc.head_dim
+    row = []
+    for x, heads, dtype, name, stride in ((q, desc.q_heads, desc.x_dtype, "q", strides[0]),
+                                          (k, desc.k_heads, desc.x_dtype, "k", strides[1]),
+                                          (q_out, desc.q_heads, desc.out_dtype, "q_out", strides[2]),
+                                          (k_out, desc.k_heads, desc.out_dtype, "k_out", strides[3])):
+        row += _rows(x, T, heads * D, dtype, name, stride) if x is not None and heads else (_addr(x), 0)
+    _check(_lib.bitq_qk_rope(desc, *row[:4], _float(q_w, desc.w_dtype, "q_w", D), _float(k_w, desc.w_dtype, "k_w", D),
+                             _longs(table, desc.rot // 2, "table"), _ints(pos, T, "pos"), *row[4:], _stream(stream)))
 
 
 def norm_desc(rows: int, width: int, u_dtype: int = DT_F32, r_dtype: int = DT_F32, w_dtype: int = DT_F32,

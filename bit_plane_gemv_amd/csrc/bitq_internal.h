@@ -213,12 +213,93 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(const bitq_attn_desc& d);
 
+// Attention of several query rows (bitq_rows.h): a workgroup's rows (32 rw),
+// waves, LDS bytes, and workgroups on a CU: two where registers (q, O and the
+// scores) and LDS leave room.
+constexpr int rows_waves(int nc, int rw) { return rw == 4 || nc <= 4 ? 4 : 2; }
+constexpr int rows_block(int rw) { return rw == 4 ? 64 : 32; }
+constexpr int rows_lds(int kv_dtype, int nc, int rw) {
+    const int es = kv_dtype == BITQ_KV_INT8 ? 1 : 2, bt = rows_block(rw), w = rows_waves(nc, rw);
+    const int stages = (rw == 4 ? 1 : w) * 2 * (2 * bt * 32 * nc * es + (es == 1 ? 8 * bt : 0));
+    const int join = rw == 4 ? 0 : w * 32 * (32 * nc + 6) * 4;
+    return stages > join ? stages : join;
+}
+constexpr int rows_groups_per_cu(int kv_dtype, int nc, bool f32, int rw) {
+    return (8 * (f32 ? 3 : 1) + 16) * nc <= 100 && rows_lds(kv_dtype, nc, rw) <= 80 * 1024 ? 2 : 1;
+}
+// How a call is split: tiles of 32 rw rows, and each one's tokens over pieces.
+struct RowsSplit {
+    int rw, tiles, pieces;
+};
+struct RowsPlan {
+    int Dp, group;
+    RowsSplit main, own;   // own: bitq_shared_attn's second part (each request's own tokens)
+    int all;               // partial results of a row (0: written whole)
+    size_t off_part, ws_bytes;
+};
+RowsPlan prompt_plan(const bitq_prompt_desc& d);
+RowsPlan shared_plan(const bitq_shared_desc& d);
+
 struct W8A8Plan {
     int kernel;            // which kernel (bitq_w8a8.hip)
     int splits;
     size_t ws_bytes;
 };
 W8A8Plan w8a8_plan(const bitq_w8a8_desc& d);
+
+struct RowsCall {
+    const void* q;
+    int64_t q_stride;
+    const void* cache;
+    const int32_t *table, *start, *lens, *prefix;
+    void* out;
+    float* lse;
+    void* ws;
+};
+int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream);
+int launch_shared_attn(const bitq_shared_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream);
+struct RowsArgs;
+void launch_rows_bf16(const RowsArgs& a, int nc, bool f32, int rw, unsigned grid, void* stream);
+void launch_rows_int8(const RowsArgs& a, int nc, bool f32, int rw, unsigned grid, void* stream);
+
+// Byte layouts of the result buffer and of the workspace of bitq_kv_fork and
+// bitq_kv_compact (bitq_pages.hip).
+constexpr int kPagesSegment = 8192;      // pages of the pool that a workgroup sums
+constexpr int kPagesSmallPool = 40000;   // one workgroup keeps a word for each page in LDS
+static_assert(4 * kPagesSmallPool + 256 <= 160 * 1024, "the words fit the LDS");
+struct KvPagesLayout {
+    size_t off_len, off_frm, off_to, total;           // result
+    size_t off_sums, off_fresh, off_rank, ws_total;   // workspace
+};
+inline KvPagesLayout kv_pages_layout(const bitq_kv_pages_desc& d) {
+    KvPagesLayout L{};
+    L.off_len = 256;
+    L.off_frm = L.off_len + align256(4 * static_cast<size_t>(d.requests));
+    L.off_to = L.off_frm + align256(4 * static_cast<size_t>(d.moves));
+    L.total = L.off_to + align256(4 * static_cast<size_t>(d.moves));
+    L.off_sums = align256(4 * static_cast<size_t>(d.pool));
+    L.off_fresh = L.off_sums + align256(4 * ((static_cast<size_t>(d.pool) + kPagesSegment - 1) / kPagesSegment));
+    L.off_rank = L.off_fresh + align256(4 * static_cast<size_t>(d.requests));
+    L.ws_total = L.off_rank + align256(4 * static_cast<size_t>(d.pool));
+    return L;
+}
+// Whether one workgroup does it all (one launch instead of four or five).
+inline bool kv_pages_small(const bitq_kv_pages_desc& d) {
+    return d.pool <= kPagesSmallPool && static_cast<int64_t>(d.requests) * d.table_stride <= 32768 && d.moves <= 65536;
+}
+
+int launch_kv_fork(const bitq_kv_pages_desc& d, const int32_t* src, const int32_t* keep, const int32_t* len, int32_t* ring,
+                   const int32_t* state, const int32_t* table, int32_t* table_out, void* result, void* ws, void* stream);
+int launch_kv_compact(const bitq_kv_pages_desc& d, const int32_t* len, const int32_t* table, int32_t* table_out, int32_t* ring,
+                      void* result, void* ws, void* stream);
+int launch_kv_copy(const bitq_kvdesc& kv, const int32_t* frm, const int32_t* to, int moves, void* cache, void* stream);
+struct RopeRows {
+    const void* at;
+    int heads;
+    int64_t stride;        // elements between tokens
+};
+int launch_qk_rope(const bitq_rope_desc& d, const RopeRows (&rows)[4] /* q, k, and their outputs */, const void* qw,
+                   const void* kw, const uint64_t* table, const int32_t* pos, void* stream);
 
 int launch_kv_plan(const bitq_kv_plan_desc& d, const int32_t* old_len, const int32_t* new_len, int32_t* ring,
                    const int32_t* state, int32_t* table, void* plan, void* stream);

@@ -1,0 +1,133 @@
+// Attention of several query rows: launches of bitq_prompt_attn and
+// bitq_shared_attn, and the kernel that joins what they split.
+#include "bitq_rows.h"
+
+namespace bitq {
+
+// Joins a row's partial results, a wave to a row: lane p has m and l of piece p
+// (at most 64), the accumulators are added with the weights 2^(m - M), AHEAD
+// pieces' loads at a time.  Bound by latency.
+template <int NE>
+__global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs a, int Dp) {
+    constexpr int AHEAD = 4;
+    const int lane = threadIdx.x & 63;
+    const uint32_t row = blockIdx.x * 4u + static_cast<uint32_t>(wave_uniform(threadIdx.x >> 6));
+    if (row >= static_cast<uint32_t>(a.T) * a.A) return;
+    const int t = row / static_cast<uint32_t>(a.A);
+    int p0 = 0;
+    if (a.mode == kRowsPrompt) {
+        if (t < rows_start(a, 0) || t >= rows_start(a, a.R)) return;  // (no request's row)
+    } else {
+        const int g = wave_search(a.groups, t, [&](int i) { return rows_start(a, i); });
+        if (g < 0 || t >= rows_start(a, g + 1)) p0 = a.piece0;  // (in no group: its own tokens alone)
+    }
+    const int n = a.all - p0;
+    const float2 ml = a.ml[static_cast<size_t>(row) * a.all + p0 + min(lane, n - 1)];
+    const bool has = lane < n && ml.y != 0.0f;  // (an l of NaN counts)
+    float M = has ? ml.x : -FLT_MAX;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    const float w = has ? __builtin_amdgcn_exp2f(ml.x - M) : 0.0f;
+    float L = has ? ml.y * w : 0.0f;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) L += __shfl_xor(L, o, 64);
+    const uint64_t some = __ballot(has);
+    float acc[NE] = {};
+    const float* base = a.part + (static_cast<size_t>(row) * a.all + p0) * Dp;
+    for (int p = 0; p < n; p += AHEAD) {
+        float v[AHEAD][NE];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+            for (int e = 0; e < NE; ++e) v[q][e] = base[min(p + q, n - 1) * Dp + min(lane + 64 * e, Dp - 1)];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            const bool use = p + q < n && (some >> min(p + q, 63) & 1);  // (a piece without tokens has written no accumulator)
+            const float wq = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), min(p + q, 63)));
+#pragma unroll
+            for (int e = 0; e < NE; ++e) acc[e] += use ? v[q][e] * wq : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+        const int d = lane + 64 * e;
+        if (d < a.D) rows_store(a, static_cast<size_t>(row) * a.D + d, L == 0.0f ? 0.0f : acc[e] / L);
+    }
+    if (lane == 0 && a.lse) a.lse[row] = rows_lse(M, L);
+}
+
+static RowsArgs rows_args(const bitq_kvdesc& kv, const RowsPlan& plan, const RowsCall& c, int heads, int q_dtype, int out_dtype,
+                          float scale) {
+    const KvLayout L = kv_layout(kv);
+    RowsArgs a{};
+    a.q = c.q;
+    a.cache = static_cast<const uint8_t*>(c.cache);
+    a.table = c.table, a.start = c.start, a.lens = c.lens, a.prefix = c.prefix;
+    a.out = c.out;
+    a.lse = c.lse;
+    a.ml = static_cast<float2*>(c.ws);
+    a.part = plan.all ? reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + plan.off_part) : nullptr;
+    a.q_stride = c.q_stride;
+    a.off_v = L.off_v, a.off_ks = L.off_ks, a.off_vs = L.off_vs;
+    a.H = kv.kv_heads, a.A = heads, a.G = plan.group, a.D = kv.head_dim;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(kv.page));
+    a.pages = kv.pages;
+    a.all = plan.all;
+    // (a scale of 0 weighs all tokens alike: so does one so small that no score counts)
+    const float s = scale * 1.44269504088896340736f, mag = s < 0 ? -s : s;
+    a.c = mag > FLT_MIN ? mag : FLT_MIN;
+    a.negative = s < 0;
+    a.odt = out_dtype;
+    a.q32 = q_dtype == BITQ_DT_F32;
+    const int per16 = q_dtype == BITQ_DT_F32 ? 4 : 8;
+    a.qvec = a.D % 8 == 0 && c.q_stride % per16 == 0 && aligned(c.q, 16);
+    a.ovec = a.D % 8 == 0 && aligned(c.out, 16);
+    return a;
+}
+
+static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, const RowsSplit& s, bool f32, void* stream) {
+    const unsigned grid = static_cast<unsigned>(s.tiles) * s.pieces * a.H;
+    if (kv.dtype == BITQ_KV_BF16) launch_rows_bf16(a, (a.D + 31) / 32, f32, s.rw, grid, stream);
+    else launch_rows_int8(a, (a.D + 31) / 32, f32, s.rw, grid, stream);
+}
+
+static void launch_rows_join(const RowsArgs& a, int Dp, void* stream) {
+    const dim3 grid((static_cast<unsigned>(a.T) * a.A + 3) / 4), block(256);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (Dp <= 64) hipLaunchKernelGGL((rows_join_kernel<1>), grid, block, 0, st, a, Dp);
+    else if (Dp <= 128) hipLaunchKernelGGL((rows_join_kernel<2>), grid, block, 0, st, a, Dp);
+    else hipLaunchKernelGGL((rows_join_kernel<4>), grid, block, 0, st, a, Dp);
+}
+
+int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream) {
+    RowsArgs a = rows_args(d.kv, plan, c, d.heads, d.q_dtype, d.out_dtype, d.scale);
+    a.mode = kRowsPrompt;
+    a.R = d.requests, a.T = d.tokens;
+    a.table_stride = d.table_stride, a.max_len = d.max_len, a.window = d.window, a.sinks = d.window ? d.sinks : 0;
+    a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
+    launch_main(d.kv, a, plan.main, d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32, stream);
+    if (plan.all) launch_rows_join(a, plan.Dp, stream);
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_shared_attn(const bitq_shared_desc& s, const RowsPlan& plan, const RowsCall& c, void* stream) {
+    const bitq_attn_desc& d = s.attn;
+    RowsArgs a = rows_args(d.kv, plan, c, d.heads, d.q_dtype, d.out_dtype, d.scale);
+    const bool f32 = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    a.T = d.requests, a.groups = s.groups, a.max_prefix = s.max_prefix;
+    a.table_stride = d.table_stride, a.max_len = d.max_len;
+    a.mode = kRowsPrefix;
+    a.R = s.groups;
+    a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
+    launch_main(d.kv, a, plan.main, f32, stream);
+    a.mode = kRowsOwn;
+    a.R = d.requests;
+    a.piece0 = plan.main.pieces;
+    a.tiles = plan.own.tiles, a.pieces = plan.own.pieces;
+    a.tps = plan.own.tiles / d.requests;
+    launch_main(d.kv, a, plan.own, f32, stream);
+    launch_rows_join(a, plan.Dp, stream);
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace bitq

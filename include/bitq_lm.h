@@ -1,9 +1,10 @@
 /*
  * bitq_lm.h -- the operators that stand between the packed linear layers of a
  * decoder: a paged key-value cache (page tables and slot maps built on the
- * GPU, cache writes, attention of one new token per request), the residual
- * update of a block with its norms, and the int8 matrix product for layers
- * kept in 8 bits.
+ * GPU, cache writes, attention of one new token per request, of several, and
+ * of requests that share a prefix; requests forked and pages compacted), the
+ * norms and rotation of queries and keys, the residual update of a block with
+ * its norms, and the int8 matrix product for layers kept in 8 bits.
  *
  * Conventions are those of bitq.h: the caller owns every buffer, the library
  * allocates nothing, every argument is checked before anything is enqueued
@@ -176,6 +177,253 @@ bitq_status bitq_paged_attn_workspace(const bitq_attn_desc* desc, size_t* bytes)
 bitq_status bitq_paged_attn(const bitq_attn_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
                             size_t cache_bytes, const int32_t* table_dev, const int32_t* lens_dev, void* out_dev,
                             float* lse_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* ================================== attention of several query rows */
+
+/*
+ * Attention of the new tokens of each request, one or many, over the paged
+ * cache (which holds them already):
+ *   out[i][a] = sum_t p_t V_t / sum_t p_t,  p_t = exp(scale q[i][a] . K_t)
+ * Request r's new tokens are rows start[r] .. start[r+1]-1 of q, the last
+ * n = start[r+1] - start[r] of its lens[r] tokens; row start[r] + j stands at
+ * position x = lens[r] - n + j and sees the tokens t <= x of its request: all of
+ * them, or with a window those with t > x - window and the first `sinks`
+ * tokens, which stay visible.  Query head a reads key-value head
+ * a / (heads / kv_heads).
+ */
+typedef struct {
+    bitq_kvdesc kv;
+    int32_t heads;         /* query heads, a multiple of kv_heads, <= 16384 */
+    int32_t requests;      /* R, 1 .. 8192 */
+    int32_t tokens;        /* T: rows of q, 1 .. 2^20; tokens * heads <= 2^26 */
+    int32_t table_stride;  /* entries of one request's row of the table */
+    int32_t max_len;       /* most tokens of a request, 1 .. table_stride * page */
+    int32_t window;        /* 0: all tokens; else the last `window` tokens */
+    int32_t sinks;         /* first tokens that stay visible; 0 without a window */
+    int32_t q_dtype;       /* BITQ_DT_F32 or BITQ_DT_BF16 */
+    int32_t out_dtype;     /* BITQ_DT_F32 or BITQ_DT_BF16 */
+    float scale;           /* finite */
+} bitq_prompt_desc;
+
+/* Workspace of bitq_prompt_attn: partial results where tokens are split over
+ * workgroups (0: none needed).  Its contents need no clearing and carry
+ * nothing from call to call; calls that share it must be ordered. */
+bitq_status bitq_prompt_attn_workspace(const bitq_prompt_desc* desc, size_t* bytes);
+
+/*
+ *   q_dev     [T][heads][head_dim] in q_dtype, row i starting q_stride elements
+ *             after row i-1
+ *   table_dev i32 [R][table_stride] page indices (an index outside the pool
+ *             reads page 0)
+ *   start_dev i32 [R+1], ascending (bitq_kv_plan's start); values are taken as
+ *             at least 0 and at most T, a request whose end lies before its
+ *             start has no rows
+ *   lens_dev  i32 [R] tokens of each request, its new ones included (0 ..
+ *             max_len, others count as the nearer end); rows that would stand
+ *             before position 0 see nothing
+ *   out_dev   [T][heads][head_dim] in out_dtype, contiguous
+ *   lse_dev   f32 [T][heads] log(sum_t p_t), or NULL
+ * A row that sees no token gives out = 0 and lse = -inf; rows outside
+ * start[0] .. start[R]-1 are left as they were.  Whatever the cache holds in
+ * places that a row does not see, infinities and NaN included, has no effect
+ * on it.  NaN in its own q or in keys or values that it sees gives NaN; so may
+ * an infinity there.
+ */
+bitq_status bitq_prompt_attn(const bitq_prompt_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
+                             size_t cache_bytes, const int32_t* table_dev, const int32_t* start_dev,
+                             const int32_t* lens_dev, void* out_dev, float* lse_dev, void* ws_dev, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * bitq_paged_attn for requests of which groups begin with the same tokens: the
+ * keys and values of such a prefix are read once for its group instead of once
+ * for each request.  Requests start[g] .. start[g+1]-1 are group g, and their
+ * first prefix[g] tokens are those of its first request, whose pages are read
+ * (pages may be common to the group's tables, as bitq_kv_fork leaves them, or
+ * copies).  Requests in no group have no prefix.
+ */
+typedef struct {
+    bitq_attn_desc attn;   /* window = 0; requests <= 8192 */
+    int32_t groups;        /* 1 .. requests */
+    int32_t max_prefix;    /* most tokens of a prefix, 1 .. attn.max_len */
+} bitq_shared_desc;
+
+bitq_status bitq_shared_attn_workspace(const bitq_shared_desc* desc, size_t* bytes);  /* as bitq_prompt_attn's */
+
+/*
+ * Buffers as for bitq_paged_attn, and
+ *   start_dev  i32 [groups+1], ascending, values taken as at least 0 and at
+ *              most R; a group whose end lies before its start has no requests
+ *   prefix_dev i32 [groups], 0 .. max_prefix (others count as the nearer end)
+ * A request shorter than its group's prefix sees its own length of it.
+ */
+bitq_status bitq_shared_attn(const bitq_shared_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
+                             size_t cache_bytes, const int32_t* table_dev, const int32_t* lens_dev,
+                             const int32_t* start_dev, const int32_t* prefix_dev, void* out_dev, float* lse_dev,
+                             void* ws_dev, size_t ws_bytes, void* stream);
+
+/* ============================================== pages of the cache */
+
+/*
+ * Requests forked, cut and freed, and the pool compacted.  Both calls find out
+ * from the tables and lengths alone which pages are held, so pages may be held
+ * by any number of requests (as bitq_kv_fork leaves them) and bitq_kv_plan can
+ * take further ones at any time.  bitq_kv_plan gives back the pages of a
+ * request that shrinks whoever else holds them: while pages are shared,
+ * requests are cut and freed by bitq_kv_fork.
+ */
+typedef struct {
+    int32_t requests;      /* R, 1 .. 8192 */
+    int32_t page;          /* tokens per page: a power of two, 8 .. 1024 */
+    int32_t table_stride;  /* entries of one request's row of the table; table_stride * page < 2^31 */
+    int32_t pool;          /* pages of the pool = entries of the ring; pool * page < 2^31 */
+    int32_t moves;         /* M: places of the list of page copies, 1 .. 2^28 (bitq_kv_fork: at least R) */
+} bitq_kv_pages_desc;
+
+/*
+ * The result buffer of both calls (i32 sections at multiples of 256 bytes, in
+ * this order):
+ *   state [4]  head and count of the ring after the call, page copies n, and
+ *              (fork) requests that did not get what they asked for / (compact)
+ *              pages below which every held page now lies
+ *   len   [R]  lengths after the call
+ *   frm   [M]  page copies to make in the cache of every layer, frm[i] to
+ *   to    [M]  to[i], i < n (-1 from n on): what bitq_kv_copy takes
+ */
+bitq_status bitq_kv_pages_size(const bitq_kv_pages_desc* desc, size_t* bytes);
+bitq_status bitq_kv_pages_workspace(const bitq_kv_pages_desc* desc, size_t* bytes);  /* needs no clearing */
+
+/*
+ * Request r becomes the first keep[r] tokens of request src[r] as it was before
+ * the call: src = r, keep = len leaves it; src = r, keep < len cuts it (0: frees
+ * it); another src forks from that request (the steps of a beam search, more
+ * samples of one prompt).  Whole pages are shared.  A page that a request ends
+ * inside is its own afterwards, so that new tokens can follow: it stays with
+ * the request that had it or else with the first that asks for it, and the
+ * others get copies of it in pages from the ring (also the first, if another
+ * request holds that page as a whole one).  Pages that nobody holds any more go
+ * to the ring's end, in order of their index.
+ *   src_dev, keep_dev, len_dev  i32 [R]; len outside 0 .. table_stride * page
+ *                counts as the nearer end
+ *   ring_dev     i32 [pool], state_dev i32 [2 or more] head, count: as for
+ *                bitq_kv_plan; ring_dev is updated in place
+ *   table_dev    i32 [R][table_stride]; table_out_dev the same, receives the
+ *                tables after the call (entries past a request's pages are left
+ *                as they were)
+ *   result_dev   bitq_kv_pages_size bytes, ws_dev bitq_kv_pages_workspace
+ *                bytes, both 256-byte aligned
+ * src outside 0 .. R-1, or keep outside 0 .. len[src]: the request stays as it
+ * was.  Copies are granted in order of the requests' index; one that the ring
+ * has no page for ends at its last whole page instead (its len says so).
+ * Both count in state[3].  Page indices outside the pool are handed on and
+ * otherwise ignored.  A repeated call on the same arguments gives the same result.
+ * The outputs may not overlap the inputs or each other (but ring_dev).
+ */
+bitq_status bitq_kv_fork(const bitq_kv_pages_desc* desc, const int32_t* src_dev, const int32_t* keep_dev,
+                         const int32_t* len_dev, int32_t* ring_dev, const int32_t* state_dev, const int32_t* table_dev,
+                         int32_t* table_out_dev, void* result_dev, size_t result_bytes, void* ws_dev, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Moves held pages to the pool's low end: the highest held page to the lowest
+ * free place, the next to the next, while that lies below it and the M places
+ * of the list last.  With M >= pool the held pages are then 0 .. n-1 (and the
+ * pool's upper part can be used otherwise).
+ *   len_dev, table_dev, table_out_dev, result_dev, ws_dev  as for bitq_kv_fork
+ *   ring_dev  i32 [pool]: receives the pages that no request holds, in order, from
+ *             place 0 (entries past them are left as they were)
+ */
+bitq_status bitq_kv_compact(const bitq_kv_pages_desc* desc, const int32_t* len_dev, const int32_t* table_dev,
+                            int32_t* table_out_dev, int32_t* ring_dev, void* result_dev, size_t result_bytes,
+                            void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
+ * Copies pages of one layer's cache (keys, values and scales): page frm[i] to
+ * page to[i], i < moves.  Pairs with an index outside the pool are skipped.
+ * No page may be copied to twice in a call, or be both copied from and to.
+ *   frm_dev, to_dev i32 [moves]; cache_dev 256-byte aligned
+ * moves = 0 does nothing.
+ */
+bitq_status bitq_kv_copy(const bitq_kvdesc* kv, const int32_t* frm_dev, const int32_t* to_dev, int32_t moves,
+                         void* cache_dev, size_t cache_bytes, void* stream);
+
+/* ================================= queries and keys: norms and positions */
+
+typedef enum {
+    BITQ_ROPE_HALF = 0,   /* pairs (x[i], x[i + rot/2]) */
+    BITQ_ROPE_PAIRS = 1   /* pairs (x[2i], x[2i + 1]) */
+} bitq_rope_layout;
+
+/*
+ * Frequencies of the rotation: pair i turns by f_i radians per position,
+ * f_i = base^(-2i/rot), stretched for contexts longer than the trained ones by
+ * dividing by `factor`
+ *   BITQ_ROPE_PLAIN   none
+ *   BITQ_ROPE_LINEAR  all of them
+ *   BITQ_ROPE_RAMP    by the pairs' numbers: d(x) = rot ln(trained / (2 pi x)) /
+ *                     (2 ln base) is where a pair makes x turns over the trained
+ *                     positions; t = clamp((i - lo) / (hi - lo), 0, 1) with lo =
+ *                     max(floor(d(turns_keep)), 0), hi = min(ceil(d(turns_scale)),
+ *                     rot - 1) (hi - lo at least 0.001): f (1 - t) + f / factor t
+ *   BITQ_ROPE_BAND    by the turns themselves: t = clamp((trained f / (2 pi) -
+ *                     turns_scale) / (turns_keep - turns_scale), 0, 1):
+ *                     f t + f / factor (1 - t)
+ */
+typedef enum { BITQ_ROPE_PLAIN = 0, BITQ_ROPE_LINEAR = 1, BITQ_ROPE_RAMP = 2, BITQ_ROPE_BAND = 3 } bitq_rope_kind;
+typedef struct {
+    int32_t rot;           /* elements of a head that are rotated: even, 2 .. 256 */
+    int32_t kind;          /* bitq_rope_kind */
+    double base;           /* > 1 */
+    double factor;         /* > 0; not for BITQ_ROPE_PLAIN */
+    double trained;        /* > 0, turns_keep > turns_scale > 0; BITQ_ROPE_RAMP and _BAND */
+    double turns_keep, turns_scale;
+} bitq_rope_freq;
+
+/*
+ * Host only.  table receives rot/2 entries: the fraction of a turn per position
+ * as a 64-bit fixed-point number, round(f_i / (2 pi) 2^64) mod 2^64 (a program
+ * with frequencies of its own fills the table in itself).  Angles are then
+ * exact to 2^-32 turns at every position below 2^31.
+ */
+bitq_status bitq_rope_table(const bitq_rope_freq* freq, uint64_t* table);
+
+/*
+ * Queries and keys of new tokens, head by head:
+ *   x' = w (.) x / sqrt(mean(x^2) + eps)   (x' = x without w)
+ * and the first rot elements of x' rotated, each pair (u, v) by its angle
+ * a = position * f_i:
+ *   (mscale (u cos a - v sin a), mscale (v cos a + u sin a))
+ */
+typedef struct {
+    int32_t tokens;        /* T, 1 .. 2^24; tokens * (q_heads + k_heads) <= 2^28 */
+    int32_t q_heads, k_heads;  /* 0 .. 16384, not both 0 */
+    int32_t head_dim;      /* 1 .. 256 */
+    int32_t rot;           /* even, 0 .. head_dim (0: norms only) */
+    int32_t layout;        /* bitq_rope_layout */
+    int32_t x_dtype;       /* of q and k: BITQ_DT_F32 or BITQ_DT_BF16 */
+    int32_t out_dtype;     /* of the outputs */
+    int32_t w_dtype;       /* of the norms' weights */
+    float eps, mscale;     /* finite, eps >= 0 */
+} bitq_rope_desc;
+
+/*
+ *   q_dev [T][q_heads][head_dim], k_dev [T][k_heads][head_dim] in x_dtype
+ *         (NULL with no heads), token t starting q_stride (k_stride) elements
+ *         after token t-1 (at least heads * head_dim)
+ *   qw_dev, kw_dev [head_dim] in w_dtype, or NULL: no norm
+ *   table_dev u64 [rot/2] (bitq_rope_table; NULL with rot = 0), 8-byte aligned
+ *   pos_dev   i32 [T] positions (bitq_kv_plan's pos); the rows of a token with
+ *             a negative one are left as they were
+ *   qo_dev, ko_dev  outputs in out_dtype, with strides of their own; may be q_dev,
+ *             k_dev themselves with the same type and stride, and overlap
+ *             nothing else of the call
+ * All naturally aligned (16-byte aligned rows and parts of 8 elements are
+ * read faster).
+ */
+bitq_status bitq_qk_rope(const bitq_rope_desc* desc, const void* q_dev, int64_t q_stride, const void* k_dev,
+                         int64_t k_stride, const void* qw_dev, const void* kw_dev, const uint64_t* table_dev,
+                         const int32_t* pos_dev, void* qo_dev, int64_t qo_stride, void* ko_dev, int64_t ko_stride,
+                         void* stream);
 
 /* ================================================ residual and norms */
 
