@@ -2,6 +2,7 @@
 // kernels (bitq_kernels.hip).  Not part of the public ABI.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 
@@ -264,12 +265,12 @@ void launch_rows_int8(const RowsArgs& a, int nc, bool f32, int rw, unsigned grid
 
 // Byte layouts of the result buffer and of the workspace of bitq_kv_fork and
 // bitq_kv_compact (bitq_pages.hip).
-constexpr int kPagesSegment = 8192;      // pages of the pool that a workgroup sums
-constexpr int kPagesSmallPool = 40000;   // one workgroup keeps a word for each page in LDS
-static_assert(4 * kPagesSmallPool + 256 <= 160 * 1024, "the words fit the LDS");
+// (pages of the pool that a workgroup sums: at most 1024 segments)
+inline int kv_pages_segment(const bitq_kv_pages_desc& d) { return static_cast<int>(round_up(std::max(1024, (d.pool + 1023) / 1024), 1024)); }
+constexpr int kPagesSmallLds = 128 * 1024;   // one workgroup keeps a word for each page and the requests in LDS
 struct KvPagesLayout {
     size_t off_len, off_frm, off_to, total;           // result
-    size_t off_sums, off_fresh, off_rank, ws_total;   // workspace
+    size_t off_sums, off_fresh, off_rank, off_reqs, ws_total;   // workspace
 };
 inline KvPagesLayout kv_pages_layout(const bitq_kv_pages_desc& d) {
     KvPagesLayout L{};
@@ -278,14 +279,16 @@ inline KvPagesLayout kv_pages_layout(const bitq_kv_pages_desc& d) {
     L.off_to = L.off_frm + align256(4 * static_cast<size_t>(d.moves));
     L.total = L.off_to + align256(4 * static_cast<size_t>(d.moves));
     L.off_sums = align256(4 * static_cast<size_t>(d.pool));
-    L.off_fresh = L.off_sums + align256(4 * ((static_cast<size_t>(d.pool) + kPagesSegment - 1) / kPagesSegment));
+    L.off_fresh = L.off_sums + align256(4 * 1024);
     L.off_rank = L.off_fresh + align256(4 * static_cast<size_t>(d.requests));
-    L.ws_total = L.off_rank + align256(4 * static_cast<size_t>(d.pool));
+    L.off_reqs = L.off_rank + align256(4 * static_cast<size_t>(d.pool));
+    L.ws_total = L.off_reqs + align256(16 * static_cast<size_t>(d.requests));
     return L;
 }
 // Whether one workgroup does it all (one launch instead of four or five).
 inline bool kv_pages_small(const bitq_kv_pages_desc& d) {
-    return d.pool <= kPagesSmallPool && static_cast<int64_t>(d.requests) * d.table_stride <= 32768 && d.moves <= 65536;
+    return 4 * static_cast<int64_t>(d.pool) + 16 * static_cast<int64_t>(d.requests) <= kPagesSmallLds &&
+           static_cast<int64_t>(d.requests) * d.table_stride <= 8192 && d.moves <= 65536;
 }
 
 int launch_kv_fork(const bitq_kv_pages_desc& d, const int32_t* src, const int32_t* keep, const int32_t* len, int32_t* ring,
