@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "bitq_device.h"
 
@@ -97,12 +98,6 @@ struct RowsShape {
     static constexpr uint32_t ODD = CN % 8 == 0 ? 64 : CN % 4 == 0 ? 32 : 16;
 };
 
-// A value of a table that no kernel of this launch writes, at a place that is
-// the same for the whole wave: through the scalar cache.
-__device__ __forceinline__ int scalar_i32(const int32_t* p, size_t i) {
-    return *(reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p)) + i);
-}
-
 template <int N>
 __device__ __forceinline__ void rows_wait_copies() {
     static_assert(N < 64, "vmcnt is a 6-bit count");
@@ -116,21 +111,59 @@ __device__ __forceinline__ void rows_wait_lds() {
     __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (7 << 4));  // lgkmcnt(0)
     asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void copy_lds4(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff) {
+// 16 (4) bytes per lane from memory straight into LDS, lane l's at dst + 16 l
+// (4 l).  Written as instructions: the compiler, which cannot tell the stage that
+// is copied into from the one that is read, would wait for the copy before every
+// LDS read behind the builtin.  The kernel waits for its copies itself
+// (rows_wait_copies), and instructions that the compiler does not count only make
+// the waits that it adds for its own loads longer.  No registers are written.
+// (s_nop: a scalar written by a vector instruction is ready for a buffer
+// instruction after 5 cycles, and M0 after 1)
+__device__ __forceinline__ u32x4_t rows_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    u32x4_t r;
+    r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32)) & 0xFFFFu;
+    r[2] = bytes;
+    r[3] = 0x00020000u;  // (as in buffer_rsrc)
+    return r;
+}
+__device__ __forceinline__ uint32_t rows_lds_address(const uint8_t* shared) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, static_cast<int>(voff), 0, 0, 0);
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)shared));
+#else
+    return 0;
 #endif
+}
+template <int BYTES>
+__device__ __forceinline__ void rows_copy_lds(u32x4_t rsrc, uint32_t dst, uint32_t voff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rsrc) : "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rsrc) : "m0");
+#endif
+}
+
+// two elements as bf16, by one instruction
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t rows_round2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
 // 8 int8 codes as bf16 (exact)
 __device__ __forceinline__ bf16x8_t rows_codes(uint32_t lo, uint32_t hi) {
-    bf16x8_t v;
+    const uint32_t b[2] = {lo, hi};
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        v[e] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(lo >> (8 * e))));
-        v[4 + e] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(hi >> (8 * e))));
+        const uint32_t u = b[e >> 1] >> (16 * (e & 1));
+        w[e] = rows_round2(static_cast<float>(static_cast<int>(static_cast<int8_t>(u))),
+                           static_cast<float>(static_cast<int>(static_cast<int8_t>(u >> 8))));
     }
-    return v;
+    return __builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // x = sum of the N bf16 terms, each the rounding of what the ones before leave
@@ -140,12 +173,18 @@ __device__ __forceinline__ void rows_terms(const float* x, bf16x8_t (&t)[N]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = x[e];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t[n][e] = static_cast<__bf16>(r[e]);
-            if (n + 1 < N) r[e] -= static_cast<float>(t[n][e]);
+        for (int e = 0; e < 4; ++e) {
+            w[e] = rows_round2(r[2 * e], r[2 * e + 1]);
+            if (n + 1 < N) {
+                r[2 * e] -= __uint_as_float(w[e] << 16);
+                r[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+            }
         }
+        t[n] = __builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3]));
+    }
 }
 
 // of the two lanes 32 h + j of a column
@@ -156,6 +195,20 @@ __device__ __forceinline__ float pair_max(float v) {
 __device__ __forceinline__ float pair_sum(float v) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Order of a region's instructions (mask 8: matrix products, 2: vector, 1024:
+// transcendental, 256: LDS reads).
+// Values: the next ones' reads first, then the next weights between the products.
+template <int PRODUCTS, int READS>
+__device__ __forceinline__ void rows_schedule_values() {
+    __builtin_amdgcn_sched_group_barrier(256, READS, 0);
+#pragma unroll
+    for (int i = 0; i < PRODUCTS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(1024, (8 + PRODUCTS - 1) / PRODUCTS, 0);
+        __builtin_amdgcn_sched_group_barrier(2, (40 + PRODUCTS - 1) / PRODUCTS, 0);
+    }
 }
 
 // ---------------------------------------------------- segments and their rows
@@ -187,16 +240,12 @@ __device__ __forceinline__ void rows_store(const RowsArgs& a, size_t i, float v)
     if (a.odt == BITQ_DT_F32) static_cast<float*>(a.out)[i] = v;
     else static_cast<uint16_t*>(a.out)[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
-__device__ __forceinline__ uint32_t rows_pair(float x, float y) {
-    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)) |
-           (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(y))) << 16);
-}
 // elements d .. d + 3 of an output row (i: element 0 of the row)
 __device__ __forceinline__ void rows_store4(const RowsArgs& a, size_t i, int d, f32x4_t v) {
     if (a.ovec) {  // (D a multiple of 8)
         if (d >= a.D) return;
         if (a.odt == BITQ_DT_F32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + i + d) = v;
-        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + i + d) = make_uint2(rows_pair(v[0], v[1]), rows_pair(v[2], v[3]));
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + i + d) = make_uint2(rows_round2(v[0], v[1]), rows_round2(v[2], v[3]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -302,37 +351,64 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
     }
     const int32_t* trow_at = a.table + static_cast<size_t>(trow) * a.table_stride;
     uint8_t* const team = s_mem + (RW == 4 ? 0 : wave * 2 * Z::STAGE);
-    auto copy = [&](int b, int stage) __attribute__((always_inline)) {
-        uint8_t* dst = team + stage * Z::STAGE;
+    // Pages of a block's groups, a lane each, loaded a block ahead: its copies then wait for no table.  (Any block: tokens past
+    // the last group are its own.)
+    int pages = 0;
+    auto look_up = [&](int b) __attribute__((always_inline)) {
+        pages = trow_at[static_cast<uint32_t>(min(block_at(b) + 8 * (lane & (BT / 8 - 1)), last_group)) >> a.page_shift];
+    };
+    // A block's copies: the groups' places, then one instruction at a time, so that they can be issued between products (a
+    // row of them holds the wave up for 150 cycles each).
+    const uint8_t* const kbase = a.cache + ((static_cast<size_t>(hk) << a.page_shift) * (Dp * ES));  // this head's keys in page 0
+    const uint32_t page_bytes = (static_cast<uint32_t>(a.H) << a.page_shift) * (Dp * ES);             // (<= 2^29)
+    const uint32_t team_lds = rows_lds_address(s_mem) + (RW == 4 ? 0 : wave * 2 * Z::STAGE);
+    const int page_mask = (1 << a.page_shift) - 1, pool = a.pages;
+    const size_t off_v = a.off_v;
+    u32x4_t ck[Z::GROUPS];  // descriptors of the groups' keys
+    const uint8_t* cv[Z::GROUPS];
+    size_t crow[Z::GROUPS];
+    uint32_t cdst = 0;
+    auto aim = [&](int b, int stage) __attribute__((always_inline)) {
         const int s = block_at(b);
+        cdst = team_lds + stage * Z::STAGE;
 #pragma unroll
         for (int u = 0; u < Z::GROUPS; ++u) {
-            const int g = RW == 4 ? wave + W * u : u;
-            const int t = min(s + 8 * g, last_group);
-            const int pg = scalar_i32(trow_at, static_cast<uint32_t>(t) >> a.page_shift);
-            const uint32_t p = static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.pages) ? pg : 0;
-            const size_t row = ((static_cast<size_t>(p) * a.H + hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-            const uint8_t* at = a.cache + row * (Dp * ES);
-            const auto rk = buffer_rsrc(at, Z::GB), rv = buffer_rsrc(at + a.off_v, Z::GB);
-#pragma unroll
-            for (int i = 0; i < Z::IPG; ++i) {
-                if (Z::GB % 1024 == 0 || i + 1 < Z::IPG || lane < (Z::GB % 1024) / 16) {
-                    const uint32_t ko = RW == 4 || u % 2 == 0 ? koff[i] : koff[i] ^ Z::ODD;
-                    buffer_copy_lds16(rk, dst + g * Z::GB + i * 1024, ko);
-                    buffer_copy_lds16(rv, dst + Z::KB + g * Z::GB + i * 1024, (i * 64 + lane) * 16);
-                }
-            }
-            if constexpr (I8) {
-                const auto rks = buffer_rsrc(a.cache + a.off_ks + row * 4, 32), rvs = buffer_rsrc(a.cache + a.off_vs + row * 4, 32);
-                if (lane < 8) {
-                    copy_lds4(rks, dst + 2 * Z::KB + g * 64, lane * 4);
-                    copy_lds4(rvs, dst + 2 * Z::KB + g * 64 + 32, lane * 4);
-                }
-            }
+            const int g = RW == 4 ? wave + W * u : u, t = min(s + 8 * g, last_group);
+            const int pg = __builtin_amdgcn_readlane(pages, g);
+            const uint32_t p = static_cast<uint32_t>(pg) < static_cast<uint32_t>(pool) ? pg : 0;
+            const uint8_t* at = kbase + (static_cast<size_t>(p) * page_bytes + static_cast<uint32_t>(t & page_mask) * (Dp * ES));
+            ck[u] = rows_rsrc(at, Z::GB);
+            cv[u] = at + off_v;
+            if constexpr (I8) crow[u] = static_cast<size_t>(at - a.cache) / Dp * 4;  // (a scale of 4 bytes for a row of Dp codes)
         }
     };
+    auto copy_one = [&](int n) __attribute__((always_inline)) {  // n-th of COPIES
+        constexpr int PER = Z::COPIES / Z::GROUPS;
+        const int u = n / PER, i = n % PER, g = RW == 4 ? wave + W * u : u;
+        if (i < 2 * Z::IPG) {
+            const int part = i >> 1;
+            const bool v = i & 1;
+            // (the odd groups' keys differ in the swizzle's bit 3 of the row)
+            const uint32_t off = v ? (part * 64 + lane) * 16 : RW == 4 || u % 2 == 0 ? koff[part] : koff[part] ^ Z::ODD;
+            if (Z::GB % 1024 == 0 || part + 1 < Z::IPG || lane < (Z::GB % 1024) / 16)
+                rows_copy_lds<16>(v ? rows_rsrc(cv[u], Z::GB) : ck[u], cdst + (v ? Z::KB : 0) + g * Z::GB + part * 1024, off);
+        } else if (lane < 8) {
+            const bool v = i & 1;
+            rows_copy_lds<4>(rows_rsrc(a.cache + (v ? a.off_vs : a.off_ks) + crow[u], 32),
+                             cdst + 2 * Z::KB + g * 64 + (v ? 32 : 0), lane * 4);
+        }
+    };
+    auto copy_all = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < Z::COPIES; ++i) copy_one(i);
+    };
     const int bstep = RW == 4 ? 1 : W, bfirst = b0 + (RW == 4 ? 0 : wave);
-    if (bfirst < b1) copy(bfirst, 0);
+    if (bfirst < b1) {
+        look_up(bfirst);
+        aim(bfirst, 0);
+        copy_all();
+        look_up(bfirst + bstep);
+    }
 
     // ---- the rows' queries: operand kc holds 8 elements of the lane's row
     bf16x8_t qf[NQ][2 * NC];
@@ -388,39 +464,69 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
     const int kr = 16 * (j >> 4) + 8 * ((j >> 2) & 1) + 4 * ((j >> 3) & 1) + (j & 3);  // token of row j of a score tile
     const int krow = kr * (Dp * ES), ksw = Z::swizzle(kr);
 
-    auto compute = [&](int s, int stage, bool edge) __attribute__((always_inline)) {
+    // Which tokens of the block at s this lane's row sees: bit 8 t + e is token s + 16 t + 8 h + e.
+    auto seen = [&](int s) __attribute__((always_inline)) {
+        auto below = [&](int limit) __attribute__((always_inline)) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int t = 0; t < T16; ++t) bits |= ((1u << min(max(limit - (s + 16 * t + 8 * h), 0), 8)) - 1u) << (8 * t);
+            return bits;
+        };
+        return below(hi) & (~below(lo) | below(sinks));
+    };
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    typedef typename std::conditional<I8, u32x2_t, u32x4_t>::type Value;
+    // One block.  The products and the softmax's instructions run side by side:
+    // a wave's weights of 16 tokens are made while the matrix cores multiply the 16
+    // before them, and operands are read from LDS well before they are needed.
+    auto compute = [&](int s, int stage, bool edge, auto copies) __attribute__((always_inline)) {
         const uint8_t* st = team + stage * Z::STAGE;
-        float x[8 * T16];
+        const float* sc = reinterpret_cast<const float*>(st + 2 * Z::KB);
+        auto value = [&](int t, int d) __attribute__((always_inline)) {  // operand: elements 32 d + j of tokens 16 t + 8 h ..
+            return *reinterpret_cast<const Value*>(st + Z::KB + ((2 * t + h) * Dp + 32 * d + j) * (8 * ES));
+        };
+        auto operand = [&](Value u) __attribute__((always_inline)) {
+            if constexpr (I8) return rows_codes(u[0], u[1]);
+            else return __builtin_bit_cast(bf16x8_t, u);
+        };
         // ---- scores of tokens s + 16 t + 8 h + e
+        constexpr int KT = BT / 32, KR = I8 ? NC : 2 * NC;  // score tiles, and reads of a tile's keys
+        constexpr int KN = KR * KT, AHEAD = KN < 8 ? KN : 8;
+        f32x16_t acc[KT];
+        u32x4_t kf[KN];
+        auto key = [&](int i) __attribute__((always_inline)) {
+            kf[i] = *reinterpret_cast<const u32x4_t*>(st + (i % KT) * 32 * Dp * ES + krow + (((2 * (i / KT) + h) ^ ksw) << 4));
+        };
 #pragma unroll
-        for (int kt = 0; kt < BT / 32; ++kt) {
-            f32x16_t acc;
+        for (int i = 0; i < AHEAD; ++i) key(i);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-            if constexpr (!I8) {
+        for (int i = 0; i < KN; ++i) {
+            const int kt = i % KT, kr_ = i / KT;
 #pragma unroll
-                for (int kc = 0; kc < 2 * NC; ++kc) {
-                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(st + kt * 32 * Dp * ES + krow + (((2 * kc + h) ^ ksw) << 4));
+            for (int b = 0; b < (I8 ? 2 : 1); ++b) {
+                const bf16x8_t k8 = !I8 ? __builtin_bit_cast(bf16x8_t, kf[i])
+                                    : b ? rows_codes(kf[i][2], kf[i][3]) : rows_codes(kf[i][0], kf[i][1]);
 #pragma unroll
-                    for (int q = NQ - 1; q >= 0; --q) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[q][kc], acc, 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int kp = 0; kp < NC; ++kp) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(st + kt * 32 * Dp * ES + krow + (((2 * kp + h) ^ ksw) << 4));
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const bf16x8_t kf = b ? rows_codes(u.z, u.w) : rows_codes(u.x, u.y);
-#pragma unroll
-                        for (int q = NQ - 1; q >= 0; --q)
-                            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[q][2 * kp + b], acc, 0, 0, 0);
-                    }
+                for (int q = NQ - 1; q >= 0; --q) {
+                    const f32x16_t zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                    acc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[q][I8 ? 2 * kr_ + b : kr_],
+                                                                      kr_ == 0 && b == 0 && q == NQ - 1 ? zero : acc[kt], 0, 0, 0);
                 }
             }
+            if (i + AHEAD < KN) key(i + AHEAD);
+            if constexpr (decltype(copies)::value) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[16 * kt + e] = acc[e];
+                for (int n = Z::COPIES * i / KN; n < Z::COPIES * (i + 1) / KN; ++n) copy_one(n);
+            }
         }
-        const float* sc = reinterpret_cast<const float*>(st + 2 * Z::KB);
+        Value vf[2][NC];
+#pragma unroll
+        for (int d = 0; d < NC; ++d) vf[0][d] = value(0, d);
+        float x[8 * T16];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[16 * kt + e] = acc[kt][e];
         if constexpr (I8) {
 #pragma unroll
             for (int t = 0; t < T16; ++t) {
@@ -433,18 +539,17 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
                 }
             }
         }
-        uint32_t keep = ~0u;  // bit 8 t + e: the row sees that token
+        uint32_t keep = ~0u;
         if (edge) {
-            keep = 0;
+            asm volatile("");  // (a branch, not selects in every block)
+            keep = seen(s);
 #pragma unroll
             for (int i = 0; i < 8 * T16; ++i) {
-                const int tk = s + 16 * (i / 8) + 8 * h + i % 8;
-                const bool see = tk < hi && (tk >= lo || tk < sinks);
-                keep |= see ? 1u << i : 0u;
-                x[i] = see ? x[i] : -INFINITY;
+                const uint32_t yes = static_cast<uint32_t>(static_cast<int32_t>(keep << (31 - i)) >> 31);
+                x[i] = __uint_as_float((__float_as_uint(x[i]) & yes) | (0xFF800000u & ~yes));  // else -inf
             }
         }
-        // ---- weights
+        // ---- the running maximum
         float mx = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < 8 * T16; ++i) mx = fmaxf(mx, x[i]);
@@ -458,102 +563,138 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[d][e] *= f;
         }
+        // ---- weights of the t-th 16 tokens, as terms
+        auto weights = [&](int t, bf16x8_t (&pf)[NP]) __attribute__((always_inline)) {
+            float p[8];
 #pragma unroll
-        for (int i = 0; i < 8 * T16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -m));
-            l += x[i];
-        }
-        if constexpr (I8) {
-#pragma unroll
-            for (int t = 0; t < T16; ++t) {
+            for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * t + e], a.c, -m));
+            l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            if constexpr (I8) {
                 const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(sc + (2 * t + h) * 16 + 8);
                 const f32x4_t v1 = *reinterpret_cast<const f32x4_t*>(sc + (2 * t + h) * 16 + 12);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float w = x[8 * t + e] * (e < 4 ? v0[e & 3] : v1[e & 3]);
-                    x[8 * t + e] = !edge || (keep >> (8 * t + e) & 1) ? w : 0.0f;  // (scales of hidden tokens may be anything)
+                for (int e = 0; e < 8; ++e) p[e] *= e < 4 ? v0[e & 3] : v1[e & 3];
+                if (edge) {  // (scales of hidden tokens may be anything)
+                    asm volatile("");
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        p[e] = __uint_as_float(__float_as_uint(p[e]) & static_cast<uint32_t>(static_cast<int32_t>(keep << (31 - 8 * t - e)) >> 31));
                 }
             }
-        }
-        // ---- values
-        bool odd = false;  // edges, bf16: some value of the block is not finite
+            rows_terms<NP>(p, pf);
+        };
+        bf16x8_t pf[2][NP];
+        weights(0, pf[0]);
 #pragma unroll
         for (int t = 0; t < T16; ++t) {
-            bf16x8_t pf[NP];
-            rows_terms<NP>(x + 8 * t, pf);
+            if (t + 1 < T16) {
+#pragma unroll
+                for (int d = 0; d < NC; ++d) vf[(t + 1) & 1][d] = value(t + 1, d);
+            }
+            if (t + 1 < T16) weights(t + 1, pf[(t + 1) & 1]);
 #pragma unroll
             for (int d = 0; d < NC; ++d) {
-                bf16x8_t vf;
-                const uint8_t* vp = st + Z::KB + ((2 * t + h) * Dp + 32 * d + j) * (8 * ES);
-                if constexpr (I8) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(vp);
-                    vf = rows_codes(u.x, u.y);
-                } else {
-                    uint4 u = *reinterpret_cast<const uint4*>(vp);
-                    if (edge) {  // a hidden value times a weight of 0 must be 0: what is not finite counts as 0 here, and below
-                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                const bf16x8_t v = operand(vf[t & 1][d]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool a0 = (w[e] & 0x7F80u) == 0x7F80u, a1 = (w[e] & 0x7F800000u) == 0x7F800000u;
-                            odd = odd || a0 || a1;
-                            w[e] &= (a0 ? 0xFFFF0000u : ~0u) & (a1 ? 0x0000FFFFu : ~0u);
-                        }
-                        u = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    vf = __builtin_bit_cast(bf16x8_t, u);
-                }
-#pragma unroll
-                for (int q = NP - 1; q >= 0; --q) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[q], o[d], 0, 0, 0);
+                for (int q = NP - 1; q >= 0; --q) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[t & 1][q], o[d], 0, 0, 0);
             }
-        }
-        if constexpr (!I8) {
-            if (edge && __any(odd)) {
-                // rows that see a value that is not finite get NaN in its element: count them with the same product
-#pragma unroll
-                for (int d = 0; d < NC; ++d) {
-                    f32x16_t cnt;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) cnt[e] = 0.0f;
-#pragma unroll
-                    for (int t = 0; t < T16; ++t) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(st + Z::KB + ((2 * t + h) * Dp + 32 * d + j) * (8 * ES));
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        bf16x8_t vf, pf;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t b = e & 1 ? w[e >> 1] >> 16 : w[e >> 1];
-                            vf[e] = static_cast<__bf16>((b & 0x7F80u) == 0x7F80u ? 1.0f : 0.0f);
-                            pf[e] = static_cast<__bf16>(keep >> (8 * t + e) & 1 ? 1.0f : 0.0f);
-                        }
-                        cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, cnt, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] = cnt[e] > 0.0f ? __builtin_nanf("") : o[d][e];
-                }
-            }
+            if (t + 1 < T16) rows_schedule_values<NC * NP, NC>();
         }
     };
 
-    int stage = 0;
-    for (int b = bfirst; b < b1; b += bstep) {
+    // A hidden value times a weight of 0 must be 0: where a row does not see a token of a block, bf16 values that are not
+    // finite (int8 codes always are) are looked for, and taken out of LDS, after the rows that see one have got NaN in its
+    // element.
+    // Whether some value of the part of the block that this wave looks after is not finite:
+    constexpr int PART = Z::KB / 1024 / (RW == 4 ? W : 1);  // 16-byte pieces of a lane
+    auto part_at = [&](int stage, int i) __attribute__((always_inline)) {
+        return reinterpret_cast<u32x4_t*>(team + stage * Z::STAGE + Z::KB + (((RW == 4 ? wave : 0) * PART + i) * 64 + lane) * 16);
+    };
+    auto find_odd = [&](int stage) __attribute__((always_inline)) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < PART; ++i) {
+            const u32x4_t w = *part_at(stage, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7F80u, w[e] >> 16 & 0x7F80u));
+        }
+        return __any(most == 0x7F80u);
+    };
+    auto mark_odd = [&](int s, int stage) __attribute__((always_inline)) {  // (counted by a product)
+        const uint32_t keep = seen(s);
+#pragma unroll
+        for (int d = 0; d < NC; ++d) {
+            f32x16_t cnt = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+            for (int t = 0; t < T16; ++t) {
+                const u32x4_t w = *reinterpret_cast<const u32x4_t*>(team + stage * Z::STAGE + Z::KB + ((2 * t + h) * Dp + 32 * d + j) * 16);
+                bf16x8_t bad, see;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    bad[e] = static_cast<__bf16>((w[e >> 1] >> (16 * (e & 1)) & 0x7F80u) == 0x7F80u ? 1.0f : 0.0f);
+                    see[e] = static_cast<__bf16>(keep >> (8 * t + e) & 1 ? 1.0f : 0.0f);
+                }
+                cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bad, see, cnt, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] = cnt[e] > 0.0f ? __builtin_nanf("") : o[d][e];
+        }
+    };
+    auto clear_odd = [&](int stage) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int i = 0; i < PART; ++i) {
+            u32x4_t w = *part_at(stage, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = (w[e] & 0x7F80u) == 0x7F80u ? w[e] & 0xFFFF0000u : w[e];
+                w[e] = (w[e] & 0x7F800000u) == 0x7F800000u ? w[e] & 0x0000FFFFu : w[e];
+            }
+            *part_at(stage, i) = w;
+        }
+    };
+    // (edges of the tile: the waves of RW = 4 look for odd values together)
+    const int tile_hi = a.mode != kRowsPrefix ? (a.mode == kRowsPrompt ? thi - (min(x0 + Z::ROWS, rows) - 1) / a.G + x0 / a.G : thi)
+                        : RW == 4             ? (__syncthreads_or(hi_min < thi && mine > 0) ? 0 : thi)
+                                              : hi_min;
+    const int tile_lo = a.mode == kRowsPrompt && a.window > 0 ? max(thi - a.window, 0) : lo_max;
+
+    auto block = [&](int b, int stage, auto copies) __attribute__((always_inline)) {
         const int s = block_at(b);
         rows_wait_copies<0>();
+        rows_wait_lds();
         if constexpr (RW == 4) {
-            rows_wait_lds();
             __builtin_amdgcn_s_barrier();  // every wave's copies have landed, and the other stage is read no more
             asm volatile("" ::: "memory");
-        } else {
-            rows_wait_lds();
         }
-        if (b + bstep < b1) copy(b + bstep, stage ^ 1);
+        if constexpr (decltype(copies)::value) {
+            aim(b + bstep, stage ^ 1);
+            look_up(b + 2 * bstep);
+        }
         const bool any = mine > 0 && s < whi && (s + BT > wlo || s < sinks);
-        if (any) {
-            const bool all = s + BT <= hi_min && (s >= lo_max || s + BT <= sinks);
-            if (all) compute(s, stage, false);
-            else compute(s, stage, true);
+        if constexpr (!I8) {
+            if (!(s + BT <= tile_hi && (s >= tile_lo || s + BT <= sinks))) {
+                asm volatile("");
+                bool odd = find_odd(stage);
+                if constexpr (RW == 4) odd = __syncthreads_or(odd);
+                if (odd) {
+                    if (any) mark_odd(s, stage);
+                    rows_wait_lds();
+                    if constexpr (RW == 4) __syncthreads();
+                    clear_odd(stage);
+                    rows_wait_lds();
+                    if constexpr (RW == 4) __syncthreads();
+                }
+            }
         }
+        if (any) compute(s, stage, !(s + BT <= hi_min && (s >= lo_max || s + BT <= sinks)), copies);
+        else if constexpr (decltype(copies)::value) copy_all();
+    };
+    int stage = 0, b = bfirst;
+    for (; b + bstep < b1; b += bstep) {
+        block(b, stage, std::true_type{});
         stage ^= 1;
     }
+    if (b < b1) block(b, stage, std::false_type{});
 
     // ---- results
     l = pair_sum(l);
