@@ -91,11 +91,12 @@ struct RowsShape {
     static constexpr int JOIN = RW == 4 ? 0 : W * 32 * (ORow + 2) * 4;
     static constexpr int LDS = rows_lds(KVT, NC, RW);
     static_assert(LDS >= TEAMS * 2 * STAGE && LDS >= JOIN, "stages, then the waves' results");
-    // piece c of row r is stored at piece c ^ swizzle(r); rows 8 further on differ in ODD of a piece's offset
+    // Piece c of row r is stored at piece c ^ swizzle(r), so that any 16 rows that differ in their last 4 bits have a
+    // piece in 16 different sixteenths of the banks (256 bytes); rows 8 further on differ in ODD of a piece's offset.
     static constexpr __device__ __forceinline__ int swizzle(int r) {
-        return CN % 8 == 0 ? (r & 3) | ((r >> 3) & 1) << 2 : CN % 4 == 0 ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r >> 3) & 1;
+        return CN % 16 == 0 ? r & 15 : CN % 8 == 0 ? (r >> 1) & 7 : CN % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
     }
-    static constexpr uint32_t ODD = CN % 8 == 0 ? 64 : CN % 4 == 0 ? 32 : 16;
+    static constexpr uint32_t ODD = CN % 16 == 0 ? 128 : CN % 8 == 0 ? 64 : CN % 4 == 0 ? 32 : 16;
 };
 
 template <int N>
@@ -119,8 +120,7 @@ __device__ __forceinline__ void rows_wait_lds() {
 // the waits that it adds for its own loads longer.  No registers are written.
 // (s_nop: a scalar written by a vector instruction is ready for a buffer
 // instruction after 5 cycles, and M0 after 1)
-__device__ __forceinline__ u32x4_t rows_rsrc(const void* base, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
+__device__ __forceinline__ u32x4_t rows_rsrc(uint64_t a, uint32_t bytes) {
     u32x4_t r;
     r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
     r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32)) & 0xFFFFu;
@@ -364,37 +364,35 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
     const uint32_t team_lds = rows_lds_address(s_mem) + (RW == 4 ? 0 : wave * 2 * Z::STAGE);
     const int page_mask = (1 << a.page_shift) - 1, pool = a.pages;
     const size_t off_v = a.off_v;
-    u32x4_t ck[Z::GROUPS];  // descriptors of the groups' keys
-    const uint8_t* cv[Z::GROUPS];
-    size_t crow[Z::GROUPS];
+    uint64_t ck[Z::GROUPS];  // places of the groups' keys (values: off_v further on)
     uint32_t cdst = 0;
     auto aim = [&](int b, int stage) __attribute__((always_inline)) {
-        const int s = block_at(b);
         cdst = team_lds + stage * Z::STAGE;
+        // (a lane for each group, then into scalar registers)
+        const int t = min(block_at(b) + 8 * (lane & (BT / 8 - 1)), last_group);
+        const uint32_t p = static_cast<uint32_t>(pages) < static_cast<uint32_t>(pool) ? pages : 0;
+        const uint64_t at = reinterpret_cast<uint64_t>(kbase) + static_cast<uint64_t>(p) * page_bytes +
+                            static_cast<uint32_t>(t & page_mask) * (Dp * ES);
 #pragma unroll
         for (int u = 0; u < Z::GROUPS; ++u) {
-            const int g = RW == 4 ? wave + W * u : u, t = min(s + 8 * g, last_group);
-            const int pg = __builtin_amdgcn_readlane(pages, g);
-            const uint32_t p = static_cast<uint32_t>(pg) < static_cast<uint32_t>(pool) ? pg : 0;
-            const uint8_t* at = kbase + (static_cast<size_t>(p) * page_bytes + static_cast<uint32_t>(t & page_mask) * (Dp * ES));
-            ck[u] = rows_rsrc(at, Z::GB);
-            cv[u] = at + off_v;
-            if constexpr (I8) crow[u] = static_cast<size_t>(at - a.cache) / Dp * 4;  // (a scale of 4 bytes for a row of Dp codes)
+            const int g = RW == 4 ? wave + W * u : u;
+            ck[u] = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at), g)) |
+                    static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at >> 32), g))) << 32;
         }
     };
     auto copy_one = [&](int n) __attribute__((always_inline)) {  // n-th of COPIES
         constexpr int PER = Z::COPIES / Z::GROUPS;
         const int u = n / PER, i = n % PER, g = RW == 4 ? wave + W * u : u;
+        const bool v = i & 1;
         if (i < 2 * Z::IPG) {
             const int part = i >> 1;
-            const bool v = i & 1;
             // (the odd groups' keys differ in the swizzle's bit 3 of the row)
             const uint32_t off = v ? (part * 64 + lane) * 16 : RW == 4 || u % 2 == 0 ? koff[part] : koff[part] ^ Z::ODD;
             if (Z::GB % 1024 == 0 || part + 1 < Z::IPG || lane < (Z::GB % 1024) / 16)
-                rows_copy_lds<16>(v ? rows_rsrc(cv[u], Z::GB) : ck[u], cdst + (v ? Z::KB : 0) + g * Z::GB + part * 1024, off);
-        } else if (lane < 8) {
-            const bool v = i & 1;
-            rows_copy_lds<4>(rows_rsrc(a.cache + (v ? a.off_vs : a.off_ks) + crow[u], 32),
+                rows_copy_lds<16>(rows_rsrc(ck[u] + (v ? off_v : 0), Z::GB), cdst + (v ? Z::KB : 0) + g * Z::GB + part * 1024, off);
+        } else if (lane < 8) {  // (a scale of 4 bytes for a row of Dp codes)
+            const uint64_t row = (ck[u] - reinterpret_cast<uint64_t>(a.cache)) / Dp * 4;
+            rows_copy_lds<4>(rows_rsrc(reinterpret_cast<uint64_t>(a.cache) + (v ? a.off_vs : a.off_ks) + row, 32),
                              cdst + 2 * Z::KB + g * 64 + (v ? 32 : 0), lane * 4);
         }
     };
@@ -492,6 +490,7 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
         // ---- scores of tokens s + 16 t + 8 h + e
         constexpr int KT = BT / 32, KR = I8 ? NC : 2 * NC;  // score tiles, and reads of a tile's keys
         constexpr int KN = KR * KT, AHEAD = KN < 8 ? KN : 8;
+        constexpr int EARLY = Z::COPIES / 3;  // copies among the keys' products, the others among the values'
         f32x16_t acc[KT];
         u32x4_t kf[KN];
         auto key = [&](int i) __attribute__((always_inline)) {
@@ -516,7 +515,7 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
             if (i + AHEAD < KN) key(i + AHEAD);
             if constexpr (decltype(copies)::value) {
 #pragma unroll
-                for (int n = Z::COPIES * i / KN; n < Z::COPIES * (i + 1) / KN; ++n) copy_one(n);
+                for (int n = EARLY * i / KN; n < EARLY * (i + 1) / KN; ++n) copy_one(n);
             }
         }
         Value vf[2][NC];
@@ -592,6 +591,11 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
                 for (int d = 0; d < NC; ++d) vf[(t + 1) & 1][d] = value(t + 1, d);
             }
             if (t + 1 < T16) weights(t + 1, pf[(t + 1) & 1]);
+            if constexpr (decltype(copies)::value) {
+                constexpr int LATE = Z::COPIES - EARLY;
+#pragma unroll
+                for (int n = EARLY + LATE * t / T16; n < EARLY + LATE * (t + 1) / T16; ++n) copy_one(n);
+            }
 #pragma unroll
             for (int d = 0; d < NC; ++d) {
                 const bf16x8_t v = operand(vf[t & 1][d]);
