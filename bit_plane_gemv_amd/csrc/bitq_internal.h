@@ -217,16 +217,18 @@ AttnPlan attn_plan(const bitq_attn_desc& d);
 // Attention of several query rows (bitq_rows.h): a workgroup's rows (32 rw),
 // waves, LDS bytes, and workgroups on a CU: two where registers (q, O and the
 // scores) and LDS leave room.
-constexpr int rows_waves(int nc, int rw) { return rw == 4 || nc <= 4 ? 4 : 2; }
+constexpr int rows_waves(int rw) { return rw == 4 ? 4 : 2; }
 constexpr int rows_block(int rw) { return rw == 4 ? 64 : 32; }
 constexpr int rows_lds(int kv_dtype, int nc, int rw) {
-    const int es = kv_dtype == BITQ_KV_INT8 ? 1 : 2, bt = rows_block(rw), w = rows_waves(nc, rw);
+    const int es = kv_dtype == BITQ_KV_INT8 ? 1 : 2, bt = rows_block(rw), w = rows_waves(rw);
     const int stages = (rw == 4 ? 1 : w) * 2 * (2 * bt * 32 * nc * es + (es == 1 ? 8 * bt : 0));
     const int join = rw == 4 ? 0 : w * 32 * (32 * nc + 6) * 4;
     return stages > join ? stages : join;
 }
 constexpr int rows_groups_per_cu(int kv_dtype, int nc, bool f32, int rw) {
-    return (8 * (f32 ? 3 : 1) + 16) * nc <= 100 && rows_lds(kv_dtype, nc, rw) <= 80 * 1024 ? 2 : 1;
+    const int per_simd = (8 * (f32 ? 3 : 1) + 16) * nc <= 100 && (rw == 4 || nc <= 2) ? 2 : 1;
+    const int by_lds = 160 * 1024 / (rows_lds(kv_dtype, nc, rw) + 1024), by_waves = per_simd * 4 / rows_waves(rw);
+    return by_lds < by_waves ? by_lds : by_waves;
 }
 // How a call is split: tiles of 32 rw rows, and each one's tokens over pieces.
 struct RowsSplit {

@@ -234,7 +234,7 @@ bitq_status launched(int e) {
 // rounds of blocks or more.
 int rows_pieces(int64_t tiles, int64_t span, int kv_heads, int groups_per_cu, int rw, int nc, int64_t most) {
     const int64_t want = 256 * groups_per_cu / std::max<int64_t>(1, tiles * kv_heads);
-    const int64_t unit = rw == 4 ? 2 * rows_block(rw) : rows_block(rw) * rows_waves(nc, rw);
+    const int64_t unit = rw == 4 ? 2 * rows_block(rw) : rows_block(rw) * rows_waves(rw);
     return static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(want, most), (span + unit - 1) / unit)));
 }
 
@@ -257,7 +257,8 @@ RowsPlan prompt_plan(const bitq_prompt_desc& d) {
     const int64_t span = d.window > 0 ? std::min<int64_t>(d.max_len, int64_t(d.window) + d.sinks + 32 * p.main.rw / p.group) : d.max_len;
     // (partial results of at most 256 MB)
     const int64_t cap = std::min<int64_t>(64, (int64_t(1) << 26) / (static_cast<int64_t>(d.tokens) * d.heads * (p.Dp + 2)));
-    p.main.pieces = rows_pieces(std::max<int64_t>(1, (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), span, d.kv.kv_heads,
+    // (tiles in use: one for each request with tokens at least)
+    p.main.pieces = rows_pieces(std::max<int64_t>(std::min(d.requests, d.tokens), (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), span, d.kv.kv_heads,
                                 rows_groups_per_cu(d.kv.dtype, nc, f32, p.main.rw), p.main.rw, nc, cap);
     if (p.main.pieces > 1) {
         p.all = p.main.pieces;

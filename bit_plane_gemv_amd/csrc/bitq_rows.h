@@ -77,7 +77,7 @@ template <int KVT, int NC, bool F32, int RW>
 struct RowsShape {
     static constexpr bool I8 = KVT == BITQ_KV_INT8;
     static constexpr int Dp = 32 * NC, ES = I8 ? 1 : 2;
-    static constexpr int W = rows_waves(NC, RW);
+    static constexpr int W = rows_waves(RW);
     static constexpr int BT = rows_block(RW);  // tokens of a block
     static constexpr int ROWS = 32 * RW;
     static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
@@ -257,7 +257,7 @@ __device__ __forceinline__ float rows_lse(float m, float l) {
 }
 
 template <int KVT, int NC, bool F32, int RW>
-__global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC, F32, RW)) void rows_attn_kernel(RowsArgs a) {
+__global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F32, RW) * rows_waves(RW) + 3) / 4) void rows_attn_kernel(RowsArgs a) {
     using Z = RowsShape<KVT, NC, F32, RW>;
     constexpr bool I8 = Z::I8;
     constexpr int Dp = Z::Dp, ES = Z::ES, W = Z::W, BT = Z::BT, NQ = Z::NQ, NP = Z::NP, CN = Z::CN, T16 = BT / 16;
@@ -270,20 +270,56 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
     const int hk = id - rest * a.H, slot = a.tiles - 1 - static_cast<int>(rest / static_cast<uint32_t>(a.pieces));
     const int piece = rest % static_cast<uint32_t>(a.pieces);
     int seg, tile, s0, n;  // segment, tile of it, its first row token and their number
+    int len0 = 0;          // the segment's length (kRowsPrompt, kRowsOwn) or its first request's
+    int g0 = -1, gend = 0, gpre = 0;  // kRowsOwn: first and last request and prefix of the request's group (g0 < 0: none)
     if (a.mode == kRowsOwn) {
         seg = slot / a.tps;
         tile = slot - seg * a.tps;
         s0 = seg;
         n = 1;
+        // (up to 63 segments or groups: their starts, lengths and prefixes are loaded together, a lane each)
+        const int len_v = rows_len(a, seg);
+        if (a.groups < 64) {
+            const int v = rows_start(a, min(lane, a.groups)), pv = a.prefix[min(lane, a.groups - 1)];
+            const int c = __builtin_popcountll(__ballot(lane < a.groups && v <= seg));
+            if (c > 0) {
+                g0 = __builtin_amdgcn_readlane(v, c - 1);
+                gend = __builtin_amdgcn_readlane(v, c);
+                gpre = __builtin_amdgcn_readlane(pv, c - 1);
+            }
+        } else {
+            const int g = wave_search(a.groups, seg, [&](int i) { return rows_start(a, i); });
+            if (g >= 0) {
+                g0 = wave_uniform(rows_start(a, g));
+                gend = wave_uniform(rows_start(a, g + 1));
+                gpre = wave_uniform(a.prefix[g]);
+            }
+        }
+        len0 = wave_uniform(len_v);
+        if (g0 < 0 || seg >= gend) g0 = -1;
     } else {
         // the tiles of segment r lie from floor(start[r] G / ROWS) + r on: ceil(n G / ROWS) of them always fit
-        auto key = [&](int r) { return rows_start(a, r) * a.G / Z::ROWS + r; };
-        seg = wave_search(a.R, slot, key);
-        if (seg < 0) return;
-        seg = wave_uniform(seg);
-        s0 = wave_uniform(rows_start(a, seg));
-        n = wave_uniform(rows_start(a, seg + 1)) - s0;
-        tile = slot - (s0 * a.G / Z::ROWS + seg);
+        auto place = [&](int start, int r) { return start * a.G / Z::ROWS + r; };
+        int s1;
+        if (a.R < 64) {
+            const int v = rows_start(a, min(lane, a.R));
+            const int len_v = a.mode == kRowsPrompt ? rows_len(a, min(lane, a.R - 1)) : 0;
+            const int c = __builtin_popcountll(__ballot(lane < a.R && place(v, lane) <= slot));
+            if (c == 0) return;
+            seg = c - 1;
+            s0 = __builtin_amdgcn_readlane(v, seg);
+            s1 = __builtin_amdgcn_readlane(v, c);
+            len0 = __builtin_amdgcn_readlane(len_v, seg);
+        } else {
+            seg = wave_search(a.R, slot, [&](int r) { return place(rows_start(a, r), r); });
+            if (seg < 0) return;
+            seg = wave_uniform(seg);
+            s0 = wave_uniform(rows_start(a, seg));
+            s1 = wave_uniform(rows_start(a, seg + 1));
+            if (a.mode == kRowsPrompt) len0 = wave_uniform(rows_len(a, seg));
+        }
+        n = s1 - s0;
+        tile = slot - place(s0, seg);
         if (n <= 0 || tile * Z::ROWS >= n * a.G) return;
     }
     const int rows = n * a.G, x0 = tile * Z::ROWS;
@@ -294,7 +330,7 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
     // ---- what the rows see: tokens below hi that are not below lo, or below sinks
     int hi, lo, thi, tlo, trow, hi_min, lo_max, whi, wlo, sinks = 0;
     if (a.mode == kRowsPrompt) {
-        const int len = wave_uniform(rows_len(a, seg)), before = len - n;
+        const int before = len0 - n;
         auto low = [&](int x) { return a.window > 0 ? max(x - a.window, 0) : 0; };
         sinks = a.window > 0 ? a.sinks : 0;
         hi = before + in + 1;
@@ -314,13 +350,8 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
         hi_min = __any(valid && hi < pre) ? 0 : pre;
         trow = s0;
     } else {
-        const int g = wave_search(a.groups, seg, [&](int i) { return rows_start(a, i); });
-        int pre = 0;
-        if (g >= 0) {
-            const int first = wave_uniform(rows_start(a, g)), end = wave_uniform(rows_start(a, g + 1));
-            if (seg < end) pre = wave_uniform(group_prefix(a, g, first));
-        }
-        hi = thi = whi = hi_min = wave_uniform(rows_len(a, seg));
+        const int pre = g0 >= 0 ? min(min(max(gpre, 0), a.max_prefix), wave_uniform(rows_len(a, g0))) : 0;
+        hi = thi = whi = hi_min = len0;
         lo = tlo = wlo = lo_max = min(pre, thi);
         trow = seg;
     }
@@ -596,12 +627,13 @@ __global__ __launch_bounds__(64 * rows_waves(NC, RW), rows_groups_per_cu(KVT, NC
 #pragma unroll
                 for (int n = EARLY + LATE * t / T16; n < EARLY + LATE * (t + 1) / T16; ++n) copy_one(n);
             }
+            bf16x8_t v[NC];
 #pragma unroll
-            for (int d = 0; d < NC; ++d) {
-                const bf16x8_t v = operand(vf[t & 1][d]);
+            for (int d = 0; d < NC; ++d) v[d] = operand(vf[t & 1][d]);
 #pragma unroll
-                for (int q = NP - 1; q >= 0; --q) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[t & 1][q], o[d], 0, 0, 0);
-            }
+            for (int q = NP - 1; q >= 0; --q)  // (terms outside: a product does not wait for the one before it)
+#pragma unroll
+                for (int d = 0; d < NC; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[d], pf[t & 1][q], o[d], 0, 0, 0);
             if (t + 1 < T16) rows_schedule_values<NC * NP, NC>();
         }
     };

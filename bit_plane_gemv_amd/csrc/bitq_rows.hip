@@ -9,7 +9,7 @@ namespace bitq {
 // pieces' loads at a time.  Bound by latency.
 template <int NE>
 __global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs a, int Dp) {
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = 32 / NE;
     const int lane = threadIdx.x & 63;
     const uint32_t row = blockIdx.x * 4u + static_cast<uint32_t>(wave_uniform(threadIdx.x >> 6));
     if (row >= static_cast<uint32_t>(a.T) * a.A) return;

@@ -5,7 +5,7 @@ namespace bitq {
 
 template <int NC, bool F32>
 static void launch_rows(const RowsArgs& a, int rw, unsigned grid, hipStream_t st) {
-    const dim3 block(64 * rows_waves(NC, rw));
+    const dim3 block(64 * rows_waves(rw));
     if (rw == 4) hipLaunchKernelGGL((rows_attn_kernel<BITQ_KV_BF16, NC, F32, 4>), dim3(grid), block, 0, st, a);
     else hipLaunchKernelGGL((rows_attn_kernel<BITQ_KV_BF16, NC, F32, 1>), dim3(grid), block, 0, st, a);
 }
