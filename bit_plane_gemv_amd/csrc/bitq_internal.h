@@ -221,7 +221,8 @@ constexpr int rows_waves(int rw) { return rw == 4 ? 4 : 2; }
 constexpr int rows_block(int rw) { return rw == 4 ? 64 : 32; }
 constexpr int rows_lds(int kv_dtype, int nc, int rw) {
     const int es = kv_dtype == BITQ_KV_INT8 ? 1 : 2, bt = rows_block(rw), w = rows_waves(rw);
-    const int stages = (rw == 4 ? 1 : w) * 2 * (2 * bt * 32 * nc * es + (es == 1 ? 8 * bt : 0));
+    // (128 rows of an int8 cache: a block in bf16 behind the stages)
+    const int stages = (rw == 4 ? 1 : w) * 2 * (2 * bt * 32 * nc * es + (es == 1 ? 8 * bt : 0)) + (rw == 4 && es == 1 ? 4 * bt * 32 * nc : 0);
     const int join = rw == 4 ? 0 : w * 32 * (32 * nc + 6) * 4;
     return stages > join ? stages : join;
 }

@@ -33,7 +33,8 @@ namespace bitq {
 // for a whole copy instruction.  Keys are stored with their 16-byte pieces
 // exchanged within a row by the row's number, so that the reads of a score tile
 // (one piece of 32 rows) fall on all banks alike.
-//   RW = 4: 128 rows, 32 to each of the 4 waves, which share blocks of 64 tokens.
+//   RW = 4: 128 rows, 32 to each of the 4 waves, which share blocks of 64 tokens
+//           (an int8 block is turned into bf16 once for all of them).
 //   RW = 1: 32 rows; each wave takes every W-th block of 32 tokens for itself
 //           (no meeting of the waves until the end), and the waves' results are
 //           joined in LDS.  For few rows, where the memory is the bound.
@@ -90,12 +91,17 @@ struct RowsShape {
     static constexpr int ORow = Dp + 4;                       // floats of a row when the waves' results meet
     static constexpr int JOIN = RW == 4 ? 0 : W * 32 * (ORow + 2) * 4;
     static constexpr int LDS = rows_lds(KVT, NC, RW);
-    static_assert(LDS >= TEAMS * 2 * STAGE && LDS >= JOIN, "stages, then the waves' results");
+    // int8 rows of RW = 4 are turned into bf16 once for all waves, in LDS behind the stages; with RW = 1 each wave turns its
+    // own operands
+    static constexpr bool CONV = I8 && RW == 4, C8 = I8 && !CONV;
+    static constexpr int OES = C8 ? 1 : 2, OKB = BT * Dp * OES, OCN = Dp * OES / 16;  // as read by the products
+    static_assert(LDS >= TEAMS * 2 * STAGE + (CONV ? 2 * OKB : 0) && LDS >= JOIN, "stages, then the waves' results");
     // Piece c of row r is stored at piece c ^ swizzle(r), so that any 16 rows that differ in their last 4 bits have a
     // piece in 16 different sixteenths of the banks (256 bytes); rows 8 further on differ in ODD of a piece's offset.
-    static constexpr __device__ __forceinline__ int swizzle(int r) {
-        return CN % 16 == 0 ? r & 15 : CN % 8 == 0 ? (r >> 1) & 7 : CN % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
+    static constexpr __device__ __forceinline__ int swizzle_of(int cn, int r) {
+        return cn % 16 == 0 ? r & 15 : cn % 8 == 0 ? (r >> 1) & 7 : cn % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
     }
+    static constexpr __device__ __forceinline__ int swizzle(int r) { return swizzle_of(CN, r); }
     static constexpr uint32_t ODD = CN % 16 == 0 ? 128 : CN % 8 == 0 ? 64 : CN % 4 == 0 ? 32 : 16;
 };
 
@@ -259,7 +265,7 @@ __device__ __forceinline__ float rows_lse(float m, float l) {
 template <int KVT, int NC, bool F32, int RW>
 __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F32, RW) * rows_waves(RW) + 3) / 4) void rows_attn_kernel(RowsArgs a) {
     using Z = RowsShape<KVT, NC, F32, RW>;
-    constexpr bool I8 = Z::I8;
+    constexpr bool I8 = Z::I8, C8 = Z::C8;
     constexpr int Dp = Z::Dp, ES = Z::ES, W = Z::W, BT = Z::BT, NQ = Z::NQ, NP = Z::NP, CN = Z::CN, T16 = BT / 16;
     __shared__ __align__(16) uint8_t s_mem[Z::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6), h = lane >> 5, j = lane & 31;
@@ -445,7 +451,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
     auto queries = [&](auto load) __attribute__((always_inline)) {
 #pragma unroll
         for (int kc = 0; kc < 2 * NC; ++kc) {
-            const int d = I8 ? 32 * (kc / 2) + 16 * h + 8 * (kc % 2) : 16 * kc + 8 * h;
+            const int d = C8 ? 32 * (kc / 2) + 16 * h + 8 * (kc % 2) : 16 * kc + 8 * h;
             float f[8];
             load(d, valid && d < a.D, f);
 #pragma unroll
@@ -491,7 +497,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
     float m = -FLT_MAX, l = 0.0f;  // m in powers of two: p = 2^(c x - m)
 
     const int kr = 16 * (j >> 4) + 8 * ((j >> 2) & 1) + 4 * ((j >> 3) & 1) + (j & 3);  // token of row j of a score tile
-    const int krow = kr * (Dp * ES), ksw = Z::swizzle(kr);
+    const int krow = kr * (Dp * Z::OES), ksw = Z::swizzle_of(Z::OCN, kr);
 
     // Which tokens of the block at s this lane's row sees: bit 8 t + e is token s + 16 t + 8 h + e.
     auto seen = [&](int s) __attribute__((always_inline)) {
@@ -504,28 +510,29 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         return below(hi) & (~below(lo) | below(sinks));
     };
     typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    typedef typename std::conditional<I8, u32x2_t, u32x4_t>::type Value;
+    typedef typename std::conditional<C8, u32x2_t, u32x4_t>::type Value;
     // One block.  The products and the softmax's instructions run side by side:
     // a wave's weights of 16 tokens are made while the matrix cores multiply the 16
     // before them, and operands are read from LDS well before they are needed.
     auto compute = [&](int s, int stage, bool edge, auto copies) __attribute__((always_inline)) {
         const uint8_t* st = team + stage * Z::STAGE;
         const float* sc = reinterpret_cast<const float*>(st + 2 * Z::KB);
+        const uint8_t* ob = Z::CONV ? s_mem + 2 * Z::STAGE : st;  // operands
         auto value = [&](int t, int d) __attribute__((always_inline)) {  // operand: elements 32 d + j of tokens 16 t + 8 h ..
-            return *reinterpret_cast<const Value*>(st + Z::KB + ((2 * t + h) * Dp + 32 * d + j) * (8 * ES));
+            return *reinterpret_cast<const Value*>(ob + Z::OKB + ((2 * t + h) * Dp + 32 * d + j) * (8 * Z::OES));
         };
         auto operand = [&](Value u) __attribute__((always_inline)) {
-            if constexpr (I8) return rows_codes(u[0], u[1]);
+            if constexpr (C8) return rows_codes(u[0], u[1]);
             else return __builtin_bit_cast(bf16x8_t, u);
         };
         // ---- scores of tokens s + 16 t + 8 h + e
-        constexpr int KT = BT / 32, KR = I8 ? NC : 2 * NC;  // score tiles, and reads of a tile's keys
+        constexpr int KT = BT / 32, KR = C8 ? NC : 2 * NC;  // score tiles, and reads of a tile's keys
         constexpr int KN = KR * KT, AHEAD = KN < 8 ? KN : 8;
         constexpr int EARLY = Z::COPIES / 3;  // copies among the keys' products, the others among the values'
         f32x16_t acc[KT];
         u32x4_t kf[KN];
         auto key = [&](int i) __attribute__((always_inline)) {
-            kf[i] = *reinterpret_cast<const u32x4_t*>(st + (i % KT) * 32 * Dp * ES + krow + (((2 * (i / KT) + h) ^ ksw) << 4));
+            kf[i] = *reinterpret_cast<const u32x4_t*>(ob + (i % KT) * 32 * Dp * Z::OES + krow + (((2 * (i / KT) + h) ^ ksw) << 4));
         };
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) key(i);
@@ -533,13 +540,13 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         for (int i = 0; i < KN; ++i) {
             const int kt = i % KT, kr_ = i / KT;
 #pragma unroll
-            for (int b = 0; b < (I8 ? 2 : 1); ++b) {
-                const bf16x8_t k8 = !I8 ? __builtin_bit_cast(bf16x8_t, kf[i])
+            for (int b = 0; b < (C8 ? 2 : 1); ++b) {
+                const bf16x8_t k8 = !C8 ? __builtin_bit_cast(bf16x8_t, kf[i])
                                     : b ? rows_codes(kf[i][2], kf[i][3]) : rows_codes(kf[i][0], kf[i][1]);
 #pragma unroll
                 for (int q = NQ - 1; q >= 0; --q) {
                     const f32x16_t zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                    acc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[q][I8 ? 2 * kr_ + b : kr_],
+                    acc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[q][C8 ? 2 * kr_ + b : kr_],
                                                                       kr_ == 0 && b == 0 && q == NQ - 1 ? zero : acc[kt], 0, 0, 0);
                 }
             }
@@ -705,6 +712,26 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         if constexpr (decltype(copies)::value) {
             aim(b + bstep, stage ^ 1);
             look_up(b + 2 * bstep);
+        }
+        if constexpr (Z::CONV) {  // the codes as bf16, 16 of them at a time, with the keys' pieces exchanged anew
+            const uint8_t* st = team + stage * Z::STAGE;
+            uint8_t* ob = s_mem + 2 * Z::STAGE;
+#pragma unroll
+            for (int i = 0; i < (Z::KB / 16 + 64 * W - 1) / (64 * W); ++i) {
+                const int at = i * 64 * W + tid;
+                if (Z::KB / 16 % (64 * W) == 0 || at < Z::KB / 16) {
+                    const u32x4_t k = *reinterpret_cast<const u32x4_t*>(st + at * 16);
+                    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(st + Z::KB + at * 16);
+                    const int r = at / CN, c = 2 * ((at - r * CN) ^ Z::swizzle(r)), sw = Z::swizzle_of(Z::OCN, r);
+                    *reinterpret_cast<bf16x8_t*>(ob + r * (Dp * 2) + ((c ^ sw) << 4)) = rows_codes(k[0], k[1]);
+                    *reinterpret_cast<bf16x8_t*>(ob + r * (Dp * 2) + (((c + 1) ^ sw) << 4)) = rows_codes(k[2], k[3]);
+                    *reinterpret_cast<bf16x8_t*>(ob + Z::OKB + at * 32) = rows_codes(v[0], v[1]);
+                    *reinterpret_cast<bf16x8_t*>(ob + Z::OKB + at * 32 + 16) = rows_codes(v[2], v[3]);
+                }
+            }
+            rows_wait_lds();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
         }
         const bool any = mine > 0 && s < whi && (s + BT > wlo || s < sinks);
         if constexpr (!I8) {
