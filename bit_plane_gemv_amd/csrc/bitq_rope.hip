@@ -32,6 +32,7 @@ struct RopeArgs {
     int64_t qs, ks, qos, kos;
     int T, QH, KH, D, rot, rot_units, units, lph_shift, passes, wdt;
     int q_groups, k_groups;  // lane groups' passes per token
+    bool wvec, tvec;         // weights, table: 16-byte aligned
     float eps, mscale, inv_d;
 };
 
@@ -144,18 +145,40 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
     rope_load<XDT, VEC>(x, xrow + static_cast<int64_t>(h0) * a.D + ea, live0 ? na : 0, va);
     rope_load<XDT, VEC>(x, xrow + static_cast<int64_t>(h0) * a.D + eb, live0 ? nb : 0, vb);
     if (w) {
+        if (VEC && a.wvec) {
+            if (a.wdt == BITQ_DT_F32) {
+                rope_load<BITQ_DT_F32, VEC>(w, ea, na, wa);
+                rope_load<BITQ_DT_F32, VEC>(w, eb, nb, wb);
+            } else {
+                rope_load<BITQ_DT_BF16, VEC>(w, ea, na, wa);
+                rope_load<BITQ_DT_BF16, VEC>(w, eb, nb, wb);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wa[e] = e < na ? load_act(w, a.wdt, ea + e) : 0.0f;
-            wb[e] = e < nb ? load_act(w, a.wdt, eb + e) : 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                wa[e] = e < na ? load_act(w, a.wdt, ea + e) : 0.0f;
+                wb[e] = e < nb ? load_act(w, a.wdt, eb + e) : 0.0f;
+            }
         }
     }
     float sn[8], cs[8];
     if (turns) {
         const int pairs = PAIRS ? half - 8 * u : na;
+        uint64_t fs[8];
+        if (VEC && a.tvec && pairs >= 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const ulonglong2 v = reinterpret_cast<const ulonglong2*>(a.table + 8 * u)[e];
+                fs[2 * e] = v.x;
+                fs[2 * e + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fs[e] = a.table[8 * u + min(e, pairs - 1)];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint64_t f = a.table[8 * u + min(e, pairs - 1)];
+            const uint64_t f = fs[e];
             sincos_turns(static_cast<uint32_t>((f * static_cast<uint64_t>(static_cast<uint32_t>(pos))) >> 32), sn[e], cs[e]);
             sn[e] *= a.mscale;
             cs[e] *= a.mscale;
@@ -249,6 +272,8 @@ int launch_qk_rope(const bitq_rope_desc& d, const RopeRows (&rows)[4], const voi
     bool vec = d.head_dim % 8 == 0 && d.rot % (pairs ? 8 : 16) == 0;
     for (int i = 0; i < 4; ++i)
         vec = vec && (!rows[i].heads || (aligned(rows[i].at, 16) && rows[i].stride % (16 / (i < 2 ? es : eo)) == 0));
+    a.wvec = aligned(qw, 16) && aligned(kw, 16);
+    a.tvec = aligned(table, 16);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (d.x_dtype == BITQ_DT_F32) {
         if (d.out_dtype == BITQ_DT_F32) launch_rope_layout<BITQ_DT_F32, BITQ_DT_F32>(a, pairs, vec, grid, st);
