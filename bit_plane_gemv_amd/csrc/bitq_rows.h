@@ -52,7 +52,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-enum RowsMode { kRowsPrompt = 0, kRowsPrefix = 1, kRowsOwn = 2 };
+enum RowsMode { kRowsPrompt = 0, kRowsPrefix = 1, kRowsOwn = 2 };  // of a workgroup
 
 struct RowsArgs {
     const void* q;
@@ -64,11 +64,12 @@ struct RowsArgs {
     float2* ml;            // [T A][all pieces]: m (in powers of two), l
     int64_t q_stride;
     size_t off_v, off_ks, off_vs;
-    int mode, R, T;        // segments (requests or groups) and rows of q
+    int R, T;              // requests, rows of q (shared: one a request)
     int H, A, G, D, page_shift, pages, table_stride, max_len, window, sinks, max_prefix;
-    int tiles;             // places for tiles (an upper bound of the tiles)
-    int tps, groups;       // kRowsOwn: tiles per segment; groups
-    int pieces, piece0, all;  // pieces a tile is split into, the first one's place, and the places of a row; all = 0: no split
+    int groups;            // of requests with a common prefix (0: bitq_prompt_attn)
+    int tiles, pieces;     // places for tiles (an upper bound of the tiles) and pieces that each is split into
+    int own_tiles, own_pieces, tps;  // shared: those of the requests' own tokens, and its tiles per request
+    int all;               // partial results of a row, a prefix's pieces first; 0: no split
     float c;               // |scale| log2(e) (> 0); a negative scale turns q's sign
     bool negative, q32, qvec, ovec;  // q32: fp32 q
     int odt;
@@ -203,20 +204,6 @@ __device__ __forceinline__ float pair_sum(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// Order of a region's instructions (mask 8: matrix products, 2: vector, 1024:
-// transcendental, 256: LDS reads).
-// Values: the next ones' reads first, then the next weights between the products.
-template <int PRODUCTS, int READS>
-__device__ __forceinline__ void rows_schedule_values() {
-    __builtin_amdgcn_sched_group_barrier(256, READS, 0);
-#pragma unroll
-    for (int i = 0; i < PRODUCTS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(1024, (8 + PRODUCTS - 1) / PRODUCTS, 0);
-        __builtin_amdgcn_sched_group_barrier(2, (40 + PRODUCTS - 1) / PRODUCTS, 0);
-    }
-}
-
 // ---------------------------------------------------- segments and their rows
 __device__ __forceinline__ int rows_start(const RowsArgs& a, int i) { return min(max(a.start[i], 0), a.T); }
 __device__ __forceinline__ int rows_len(const RowsArgs& a, int i) { return min(max(a.lens[i], 0), a.max_len); }
@@ -272,13 +259,32 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
 
     // ---- the tile: heads fastest (an XCD, blockIdx % 8, then sees few heads and
     // shares their keys in its L2), last tiles first (a prompt's longest)
-    const uint32_t id = blockIdx.x, rest = id / static_cast<uint32_t>(a.H);
-    const int hk = id - rest * a.H, slot = a.tiles - 1 - static_cast<int>(rest / static_cast<uint32_t>(a.pieces));
-    const int piece = rest % static_cast<uint32_t>(a.pieces);
+    // (a launch with prefixes and the requests' own tokens: their workgroups alternate)
+    uint32_t id = blockIdx.x;
+    int mode = kRowsPrompt, tiles = a.tiles, pieces = a.pieces, piece0 = 0, segments = a.R;
+    if (a.groups > 0) {
+        const uint32_t n1 = static_cast<uint32_t>(a.tiles) * a.pieces * a.H;
+        const uint32_t before = static_cast<uint32_t>(static_cast<uint64_t>(id) * n1 / gridDim.x);
+        const uint32_t after = static_cast<uint32_t>(static_cast<uint64_t>(id + 1) * n1 / gridDim.x);
+        if (after > before) {
+            mode = kRowsPrefix;
+            id = before;
+            segments = a.groups;
+        } else {
+            mode = kRowsOwn;
+            id -= before;
+            tiles = a.own_tiles;
+            piece0 = a.pieces;
+            pieces = a.own_pieces;
+        }
+    }
+    const uint32_t rest = id / static_cast<uint32_t>(a.H);
+    const int hk = id - rest * a.H, slot = tiles - 1 - static_cast<int>(rest / static_cast<uint32_t>(pieces));
+    const int piece = rest % static_cast<uint32_t>(pieces);
     int seg, tile, s0, n;  // segment, tile of it, its first row token and their number
     int len0 = 0;          // the segment's length (kRowsPrompt, kRowsOwn) or its first request's
     int g0 = -1, gend = 0, gpre = 0;  // kRowsOwn: first and last request and prefix of the request's group (g0 < 0: none)
-    if (a.mode == kRowsOwn) {
+    if (mode == kRowsOwn) {
         seg = slot / a.tps;
         tile = slot - seg * a.tps;
         s0 = seg;
@@ -307,22 +313,22 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         // the tiles of segment r lie from floor(start[r] G / ROWS) + r on: ceil(n G / ROWS) of them always fit
         auto place = [&](int start, int r) { return start * a.G / Z::ROWS + r; };
         int s1;
-        if (a.R < 64) {
-            const int v = rows_start(a, min(lane, a.R));
-            const int len_v = a.mode == kRowsPrompt ? rows_len(a, min(lane, a.R - 1)) : 0;
-            const int c = __builtin_popcountll(__ballot(lane < a.R && place(v, lane) <= slot));
+        if (segments < 64) {
+            const int v = rows_start(a, min(lane, segments));
+            const int len_v = mode == kRowsPrompt ? rows_len(a, min(lane, segments - 1)) : 0;
+            const int c = __builtin_popcountll(__ballot(lane < segments && place(v, lane) <= slot));
             if (c == 0) return;
             seg = c - 1;
             s0 = __builtin_amdgcn_readlane(v, seg);
             s1 = __builtin_amdgcn_readlane(v, c);
             len0 = __builtin_amdgcn_readlane(len_v, seg);
         } else {
-            seg = wave_search(a.R, slot, [&](int r) { return place(rows_start(a, r), r); });
+            seg = wave_search(segments, slot, [&](int r) { return place(rows_start(a, r), r); });
             if (seg < 0) return;
             seg = wave_uniform(seg);
             s0 = wave_uniform(rows_start(a, seg));
             s1 = wave_uniform(rows_start(a, seg + 1));
-            if (a.mode == kRowsPrompt) len0 = wave_uniform(rows_len(a, seg));
+            if (mode == kRowsPrompt) len0 = wave_uniform(rows_len(a, seg));
         }
         n = s1 - s0;
         tile = slot - place(s0, seg);
@@ -335,7 +341,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
 
     // ---- what the rows see: tokens below hi that are not below lo, or below sinks
     int hi, lo, thi, tlo, trow, hi_min, lo_max, whi, wlo, sinks = 0;
-    if (a.mode == kRowsPrompt) {
+    if (mode == kRowsPrompt) {
         const int before = len0 - n;
         auto low = [&](int x) { return a.window > 0 ? max(x - a.window, 0) : 0; };
         sinks = a.window > 0 ? a.sinks : 0;
@@ -348,7 +354,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         wlo = low(hi_min);
         lo_max = low(whi);
         trow = seg;
-    } else if (a.mode == kRowsPrefix) {
+    } else if (mode == kRowsPrefix) {
         const int pre = wave_uniform(group_prefix(a, seg, s0));
         hi = min(rows_len(a, tok), pre);
         lo = tlo = wlo = lo_max = 0;
@@ -374,8 +380,8 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
     if (!apart) first_blocks = 0;
     const int base = apart || sinks == 0 ? base0 : 0;
     const int blocks = thi > base ? first_blocks + (thi - base + BT - 1) / BT : 0;
-    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * piece / a.pieces);
-    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (piece + 1) / a.pieces);
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * piece / pieces);
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (piece + 1) / pieces);
     const int last_group = max(thi - 1, 0) & ~7;
     auto block_at = [&](int b) { return b < first_blocks ? b * BT : base + (b - first_blocks) * BT; };
 
@@ -528,7 +534,6 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         // ---- scores of tokens s + 16 t + 8 h + e
         constexpr int KT = BT / 32, KR = C8 ? NC : 2 * NC;  // score tiles, and reads of a tile's keys
         constexpr int KN = KR * KT, AHEAD = KN < 8 ? KN : 8;
-        constexpr int EARLY = Z::COPIES / 3;  // copies among the keys' products, the others among the values'
         f32x16_t acc[KT];
         u32x4_t kf[KN];
         auto key = [&](int i) __attribute__((always_inline)) {
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
             if (i + AHEAD < KN) key(i + AHEAD);
             if constexpr (decltype(copies)::value) {
 #pragma unroll
-                for (int n = EARLY * i / KN; n < EARLY * (i + 1) / KN; ++n) copy_one(n);
+                for (int n = Z::COPIES * i / KN; n < Z::COPIES * (i + 1) / KN; ++n) copy_one(n);
             }
         }
         Value vf[2][NC];
@@ -586,7 +591,8 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
                 x[i] = __uint_as_float((__float_as_uint(x[i]) & yes) | (0xFF800000u & ~yes));  // else -inf
             }
         }
-        // ---- the running maximum
+        // ---- the running maximum.  (The wave that has products to issue goes first: 208 -> 199 us for a prompt of 4096.)
+        __builtin_amdgcn_s_setprio(0);
         float mx = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < 8 * T16; ++i) mx = fmaxf(mx, x[i]);
@@ -622,6 +628,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         };
         bf16x8_t pf[2][NP];
         weights(0, pf[0]);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int t = 0; t < T16; ++t) {
             if (t + 1 < T16) {
@@ -629,11 +636,6 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
                 for (int d = 0; d < NC; ++d) vf[(t + 1) & 1][d] = value(t + 1, d);
             }
             if (t + 1 < T16) weights(t + 1, pf[(t + 1) & 1]);
-            if constexpr (decltype(copies)::value) {
-                constexpr int LATE = Z::COPIES - EARLY;
-#pragma unroll
-                for (int n = EARLY + LATE * t / T16; n < EARLY + LATE * (t + 1) / T16; ++n) copy_one(n);
-            }
             bf16x8_t v[NC];
 #pragma unroll
             for (int d = 0; d < NC; ++d) v[d] = operand(vf[t & 1][d]);
@@ -641,7 +643,6 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
             for (int q = NP - 1; q >= 0; --q)  // (terms outside: a product does not wait for the one before it)
 #pragma unroll
                 for (int d = 0; d < NC; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[d], pf[t & 1][q], o[d], 0, 0, 0);
-            if (t + 1 < T16) rows_schedule_values<NC * NP, NC>();
         }
     };
 
@@ -696,10 +697,10 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         }
     };
     // (edges of the tile: the waves of RW = 4 look for odd values together)
-    const int tile_hi = a.mode != kRowsPrefix ? (a.mode == kRowsPrompt ? thi - (min(x0 + Z::ROWS, rows) - 1) / a.G + x0 / a.G : thi)
+    const int tile_hi = mode != kRowsPrefix ? (mode == kRowsPrompt ? thi - (min(x0 + Z::ROWS, rows) - 1) / a.G + x0 / a.G : thi)
                         : RW == 4             ? (__syncthreads_or(hi_min < thi && mine > 0) ? 0 : thi)
                                               : hi_min;
-    const int tile_lo = a.mode == kRowsPrompt && a.window > 0 ? max(thi - a.window, 0) : lo_max;
+    const int tile_lo = mode == kRowsPrompt && a.window > 0 ? max(thi - a.window, 0) : lo_max;
 
     auto block = [&](int b, int stage, auto copies) __attribute__((always_inline)) {
         const int s = block_at(b);
@@ -774,7 +775,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
                                 f32x4_t{o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv, o[d][4 * b + 3] * inv});
             if (h == 0 && a.lse) a.lse[row_at] = rows_lse(m, l);
         } else {
-            const size_t at = row_at * a.all + a.piece0 + piece;
+            const size_t at = row_at * a.all + piece0 + piece;
             if (b0 < b1) {
 #pragma unroll
                 for (int d = 0; d < NC; ++d)
@@ -824,7 +825,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
                 rows_store4(a, ra * a.D, d, f32x4_t{acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv});
                 if (d == 0 && a.lse) a.lse[ra] = rows_lse(M, L);
             } else {
-                const size_t at = ra * a.all + a.piece0 + piece;
+                const size_t at = ra * a.all + piece0 + piece;
                 if (b0 < b1) *reinterpret_cast<f32x4_t*>(a.part + at * Dp + d) = acc;
                 if (d == 0) a.ml[at] = make_float2(M, L);
             }

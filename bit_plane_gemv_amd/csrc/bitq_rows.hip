@@ -15,11 +15,11 @@ __global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs a, int Dp) {
     if (row >= static_cast<uint32_t>(a.T) * a.A) return;
     const int t = row / static_cast<uint32_t>(a.A);
     int p0 = 0;
-    if (a.mode == kRowsPrompt) {
+    if (a.groups == 0) {
         if (t < rows_start(a, 0) || t >= rows_start(a, a.R)) return;  // (no request's row)
     } else {
         const int g = wave_search(a.groups, t, [&](int i) { return rows_start(a, i); });
-        if (g < 0 || t >= rows_start(a, g + 1)) p0 = a.piece0;  // (in no group: its own tokens alone)
+        if (g < 0 || t >= rows_start(a, g + 1)) p0 = a.pieces;  // (in no group: its own tokens alone)
     }
     const int n = a.all - p0;
     const float2 ml = a.ml[static_cast<size_t>(row) * a.all + p0 + min(lane, n - 1)];
@@ -85,10 +85,10 @@ static RowsArgs rows_args(const bitq_kvdesc& kv, const RowsPlan& plan, const Row
     return a;
 }
 
-static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, const RowsSplit& s, bool f32, void* stream) {
-    const unsigned grid = static_cast<unsigned>(s.tiles) * s.pieces * a.H;
-    if (kv.dtype == BITQ_KV_BF16) launch_rows_bf16(a, (a.D + 31) / 32, f32, s.rw, grid, stream);
-    else launch_rows_int8(a, (a.D + 31) / 32, f32, s.rw, grid, stream);
+static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, int rw, bool f32, void* stream) {
+    const unsigned grid = (static_cast<unsigned>(a.tiles) * a.pieces + static_cast<unsigned>(a.own_tiles) * a.own_pieces) * a.H;
+    if (kv.dtype == BITQ_KV_BF16) launch_rows_bf16(a, (a.D + 31) / 32, f32, rw, grid, stream);
+    else launch_rows_int8(a, (a.D + 31) / 32, f32, rw, grid, stream);
 }
 
 static void launch_rows_join(const RowsArgs& a, int Dp, void* stream) {
@@ -101,11 +101,10 @@ static void launch_rows_join(const RowsArgs& a, int Dp, void* stream) {
 
 int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream) {
     RowsArgs a = rows_args(d.kv, plan, c, d.heads, d.q_dtype, d.out_dtype, d.scale);
-    a.mode = kRowsPrompt;
     a.R = d.requests, a.T = d.tokens;
     a.table_stride = d.table_stride, a.max_len = d.max_len, a.window = d.window, a.sinks = d.window ? d.sinks : 0;
     a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
-    launch_main(d.kv, a, plan.main, d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32, stream);
+    launch_main(d.kv, a, plan.main.rw, d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32, stream);
     if (plan.all) launch_rows_join(a, plan.Dp, stream);
     return static_cast<int>(hipGetLastError());
 }
@@ -114,18 +113,19 @@ int launch_shared_attn(const bitq_shared_desc& s, const RowsPlan& plan, const Ro
     const bitq_attn_desc& d = s.attn;
     RowsArgs a = rows_args(d.kv, plan, c, d.heads, d.q_dtype, d.out_dtype, d.scale);
     const bool f32 = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
-    a.T = d.requests, a.groups = s.groups, a.max_prefix = s.max_prefix;
+    a.R = a.T = d.requests, a.groups = s.groups, a.max_prefix = s.max_prefix;
     a.table_stride = d.table_stride, a.max_len = d.max_len;
-    a.mode = kRowsPrefix;
-    a.R = s.groups;
     a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
-    launch_main(d.kv, a, plan.main, f32, stream);
-    a.mode = kRowsOwn;
-    a.R = d.requests;
-    a.piece0 = plan.main.pieces;
-    a.tiles = plan.own.tiles, a.pieces = plan.own.pieces;
-    a.tps = plan.own.tiles / d.requests;
-    launch_main(d.kv, a, plan.own, f32, stream);
+    a.own_tiles = plan.own.tiles, a.own_pieces = plan.own.pieces, a.tps = plan.own.tiles / d.requests;
+    if (plan.main.rw == plan.own.rw) {
+        launch_main(d.kv, a, plan.main.rw, f32, stream);
+    } else {
+        a.own_tiles = 0;
+        launch_main(d.kv, a, plan.main.rw, f32, stream);
+        a.tiles = 0;
+        a.own_tiles = plan.own.tiles;
+        launch_main(d.kv, a, plan.own.rw, f32, stream);
+    }
     launch_rows_join(a, plan.Dp, stream);
     return static_cast<int>(hipGetLastError());
 }
