@@ -256,7 +256,7 @@ RowsPlan prompt_plan(const bitq_prompt_desc& d) {
     p.main.tiles = static_cast<int>(rows / (32 * p.main.rw) + d.requests);
     const int64_t span = d.window > 0 ? std::min<int64_t>(d.max_len, int64_t(d.window) + d.sinks + 32 * p.main.rw / p.group) : d.max_len;
     // (partial results of at most 256 MB)
-    const int64_t cap = std::min<int64_t>(64, (int64_t(1) << 26) / (static_cast<int64_t>(d.tokens) * d.heads * (p.Dp + 2)));
+    const int64_t cap = std::min<int64_t>(512, (int64_t(1) << 26) / (static_cast<int64_t>(d.tokens) * d.heads * (p.Dp + 2)));
     // (tiles in use: one for each request with tokens at least)
     p.main.pieces = rows_pieces(std::max<int64_t>(std::min(d.requests, d.tokens), (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), span, d.kv.kv_heads,
                                 rows_groups_per_cu(d.kv.dtype, nc, f32, p.main.rw), p.main.rw, nc, cap);
@@ -283,7 +283,7 @@ RowsPlan shared_plan(const bitq_shared_desc& s) {
     p.own.rw = p.group <= 32 ? 1 : 4;
     p.own.tiles = d.requests * ((p.group + 32 * p.own.rw - 1) / (32 * p.own.rw));
     // (partial results of at most 256 MB; 2^23 rows: one piece of each)
-    const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(32, (int64_t(1) << 25) / (static_cast<int64_t>(d.requests) * d.heads * (p.Dp + 2))));
+    const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(512, (int64_t(1) << 25) / (static_cast<int64_t>(d.requests) * d.heads * (p.Dp + 2))));
     p.main.pieces = rows_pieces(std::max<int64_t>(s.groups, (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), s.max_prefix, H,
                                 rows_groups_per_cu(d.kv.dtype, nc, f32, p.main.rw), p.main.rw, nc, cap);
     p.own.pieces = rows_pieces(p.own.tiles, std::max(d.max_len - s.max_prefix, 1), H,

@@ -4,14 +4,18 @@
 
 namespace bitq {
 
-// Joins a row's partial results, a wave to a row: lane p has m and l of piece p
-// (at most 64), the accumulators are added with the weights 2^(m - M), AHEAD
-// pieces' loads at a time.  Bound by latency.
-template <int NE>
-__global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs a, int Dp) {
+// Joins a row's partial results: NW waves to a row, each with a share of its
+// pieces, 64 at a time: lane p has m and l of piece p, the accumulators are added
+// with the weights 2^(m - M), AHEAD pieces' loads on their way together.  Bound by
+// latency; one wave a row where there are many rows (4096 rows of 17 pieces, 36
+// MB, 10 us), 16 where there are few (rows of 256, 14 of 187 pieces: 29 us with
+// one).
+template <int NE, int NW>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void rows_join_kernel(RowsArgs a, int Dp) {
     constexpr int AHEAD = 32 / NE;
-    const int lane = threadIdx.x & 63;
-    const uint32_t row = blockIdx.x * 4u + static_cast<uint32_t>(wave_uniform(threadIdx.x >> 6));
+    __shared__ float s_acc[NW][64 * NE], s_m[NW], s_l[NW];
+    const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
+    const uint32_t row = NW == 1 ? blockIdx.x * 4u + static_cast<uint32_t>(wave) : blockIdx.x;
     if (row >= static_cast<uint32_t>(a.T) * a.A) return;
     const int t = row / static_cast<uint32_t>(a.A);
     int p0 = 0;
@@ -21,31 +25,62 @@ __global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs a, int Dp) {
         const int g = wave_search(a.groups, t, [&](int i) { return rows_start(a, i); });
         if (g < 0 || t >= rows_start(a, g + 1)) p0 = a.pieces;  // (in no group: its own tokens alone)
     }
-    const int n = a.all - p0;
-    const float2 ml = a.ml[static_cast<size_t>(row) * a.all + p0 + min(lane, n - 1)];
-    const bool has = lane < n && ml.y != 0.0f;  // (an l of NaN counts)
-    float M = has ? ml.x : -FLT_MAX;
+    float acc[NE] = {}, M = -FLT_MAX, L = 0.0f;
+    const int per = (a.all - p0 + NW - 1) / NW, end = NW == 1 ? a.all : min(a.all, p0 + (wave + 1) * per);
+    for (int c = p0 + (NW == 1 ? 0 : wave * per); c < end; c += 64) {
+        const int n = min(64, end - c);
+        const float2 ml = a.ml[static_cast<size_t>(row) * a.all + c + min(lane, n - 1)];
+        const bool has = lane < n && ml.y != 0.0f;  // (an l of NaN counts)
+        float mn = has ? ml.x : -FLT_MAX;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
-    const float w = has ? __builtin_amdgcn_exp2f(ml.x - M) : 0.0f;
-    float L = has ? ml.y * w : 0.0f;
+        for (int o = 32; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor(mn, o, 64));
+        mn = fmaxf(M, mn);
+        const float f = __builtin_amdgcn_exp2f(M - mn), w = has ? __builtin_amdgcn_exp2f(ml.x - mn) : 0.0f;
+        M = mn;
+        float sum = has ? ml.y * w : 0.0f;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) L += __shfl_xor(L, o, 64);
-    const uint64_t some = __ballot(has);
-    float acc[NE] = {};
-    const float* base = a.part + (static_cast<size_t>(row) * a.all + p0) * Dp;
-    for (int p = 0; p < n; p += AHEAD) {
-        float v[AHEAD][NE];
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+        L = L * f + sum;
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q)
+        for (int e = 0; e < NE; ++e) acc[e] *= f;
+        const uint64_t some = __ballot(has);
+        const float* base = a.part + (static_cast<size_t>(row) * a.all + c) * Dp;
+        for (int p = 0; p < n; p += AHEAD) {
+            float v[AHEAD][NE];
 #pragma unroll
-            for (int e = 0; e < NE; ++e) v[q][e] = base[min(p + q, n - 1) * Dp + min(lane + 64 * e, Dp - 1)];
+            for (int q = 0; q < AHEAD; ++q)
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            const bool use = p + q < n && (some >> min(p + q, 63) & 1);  // (a piece without tokens has written no accumulator)
-            const float wq = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), min(p + q, 63)));
+                for (int e = 0; e < NE; ++e) v[q][e] = base[min(p + q, n - 1) * Dp + min(lane + 64 * e, Dp - 1)];
 #pragma unroll
-            for (int e = 0; e < NE; ++e) acc[e] += use ? v[q][e] * wq : 0.0f;
+            for (int q = 0; q < AHEAD; ++q) {
+                const bool use = p + q < n && (some >> min(p + q, 63) & 1);  // (a piece without tokens has written no accumulator)
+                const float wq = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), min(p + q, 63)));
+#pragma unroll
+                for (int e = 0; e < NE; ++e) acc[e] += use ? v[q][e] * wq : 0.0f;
+            }
+        }
+    }
+    if constexpr (NW > 1) {
+        if (lane == 0) {
+            s_m[wave] = M;
+            s_l[wave] = L;
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s_acc[wave][lane + 64 * e] = acc[e];
+        __syncthreads();
+        if (wave != 0) return;
+        M = s_m[0];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) M = fmaxf(M, s_m[v]);
+        L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) {
+            const float f = __builtin_amdgcn_exp2f(s_m[v] - M);
+            L += f * s_l[v];
+#pragma unroll
+            for (int e = 0; e < NE; ++e) acc[e] += f * s_acc[v][lane + 64 * e];
         }
     }
 #pragma unroll
@@ -91,12 +126,17 @@ static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, int rw, bool f
     else launch_rows_int8(a, (a.D + 31) / 32, f32, rw, grid, stream);
 }
 
+template <int NE>
+static void launch_rows_join(const RowsArgs& a, int Dp, hipStream_t st) {
+    const unsigned rows = static_cast<unsigned>(a.T) * a.A;
+    if (rows <= 1024 && a.all > 8) hipLaunchKernelGGL((rows_join_kernel<NE, 16>), dim3(rows), dim3(1024), 0, st, a, Dp);
+    else hipLaunchKernelGGL((rows_join_kernel<NE, 1>), dim3((rows + 3) / 4), dim3(256), 0, st, a, Dp);
+}
 static void launch_rows_join(const RowsArgs& a, int Dp, void* stream) {
-    const dim3 grid((static_cast<unsigned>(a.T) * a.A + 3) / 4), block(256);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (Dp <= 64) hipLaunchKernelGGL((rows_join_kernel<1>), grid, block, 0, st, a, Dp);
-    else if (Dp <= 128) hipLaunchKernelGGL((rows_join_kernel<2>), grid, block, 0, st, a, Dp);
-    else hipLaunchKernelGGL((rows_join_kernel<4>), grid, block, 0, st, a, Dp);
+    if (Dp <= 64) launch_rows_join<1>(a, Dp, st);
+    else if (Dp <= 128) launch_rows_join<2>(a, Dp, st);
+    else launch_rows_join<4>(a, Dp, st);
 }
 
 int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream) {
