@@ -234,7 +234,7 @@ bitq_status launched(int e) {
 // rounds of blocks or more.
 int rows_pieces(int64_t tiles, int64_t span, int kv_heads, int groups_per_cu, int rw, int nc, int64_t most) {
     const int64_t want = 256 * groups_per_cu / std::max<int64_t>(1, tiles * kv_heads);
-    const int64_t unit = 2 * rows_block(rw) * (rw == 4 ? 1 : rows_waves(rw));
+    const int64_t unit = rows_block(rw) * 2;  // (128 rows: two blocks; few rows: a block for each of the two waves)
     return static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(want, most), (span + unit - 1) / unit)));
 }
 
