@@ -320,7 +320,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
             }
         }
         len0 = wave_uniform(len_v);
-        if (g0 < 0 || seg >= gend) g0 = -1;
+        if (g0 > seg || seg >= gend) g0 = -1;  // (later groups: only where starts do not ascend)
     } else {
         // the tiles of segment r lie from floor(start[r] G / ROWS) + r on: ceil(n G / ROWS) of them always fit
         auto place = [&](int start, int r) { return start * a.G / Z::ROWS + r; };
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         }
         n = s1 - s0;
         tile = slot - place(s0, seg);
-        if (n <= 0 || tile * Z::ROWS >= n * a.G) return;
+        if (n <= 0 || tile < 0 || tile * Z::ROWS >= n * a.G) return;
     }
     const int rows = n * a.G, x0 = tile * Z::ROWS;
     const int xw = x0 + (RW == 4 ? 32 * wave : 0), mine = min(32, rows - xw);  // this wave's rows (may be none)
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
     int hi, lo, thi, tlo, trow, hi_min, lo_max, whi, wlo, sinks = 0;
     if (mode == kRowsPrompt) {
         const int before = len0 - n;
-        auto low = [&](int x) { return a.window > 0 ? max(x - a.window, 0) : 0; };
+        auto low = [&](int x) { return a.window > 0 && x > a.window ? x - a.window : 0; };  // (x may be negative)
         sinks = a.window > 0 ? a.sinks : 0;
         hi = before + in + 1;
         lo = low(hi);
@@ -712,7 +712,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
     const int tile_hi = mode != kRowsPrefix ? (mode == kRowsPrompt ? thi - (min(x0 + Z::ROWS, rows) - 1) / a.G + x0 / a.G : thi)
                         : RW == 4             ? (__syncthreads_or(hi_min < thi && mine > 0) ? 0 : thi)
                                               : hi_min;
-    const int tile_lo = mode == kRowsPrompt && a.window > 0 ? max(thi - a.window, 0) : lo_max;
+    const int tile_lo = mode == kRowsPrompt && a.window > 0 ? (thi > a.window ? thi - a.window : 0) : lo_max;
 
     auto block = [&](int b, int stage, auto copies) __attribute__((always_inline)) {
         const int s = block_at(b);

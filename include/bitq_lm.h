@@ -217,7 +217,8 @@ bitq_status bitq_prompt_attn_workspace(const bitq_prompt_desc* desc, size_t* byt
  *             reads page 0)
  *   start_dev i32 [R+1], ascending (bitq_kv_plan's start); values are taken as
  *             at least 0 and at most T, a request whose end lies before its
- *             start has no rows
+ *             start has no rows.  (Where they do not ascend, the results are
+ *             undefined; no access leaves the buffers.)
  *   lens_dev  i32 [R] tokens of each request, its new ones included (0 ..
  *             max_len, others count as the nearer end); rows that would stand
  *             before position 0 see nothing
@@ -254,6 +255,7 @@ bitq_status bitq_shared_attn_workspace(const bitq_shared_desc* desc, size_t* byt
  * Buffers as for bitq_paged_attn, and
  *   start_dev  i32 [groups+1], ascending, values taken as at least 0 and at
  *              most R; a group whose end lies before its start has no requests
+ *              (where they do not ascend, as for bitq_prompt_attn)
  *   prefix_dev i32 [groups], 0 .. max_prefix (others count as the nearer end)
  * A request shorter than its group's prefix sees its own length of it.
  */

@@ -123,6 +123,12 @@ def test_prompt_rows_before_position_zero_see_nothing():
     check_prompt([6, 4, 50], [2, 0, 20], 2, 3, 64, 16, "int8", "bf16", window=3, sinks=1)
 
 
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 9, 3)])
+def test_prompt_widest_windows(window, sinks):
+    """Also for rows before position 0 in a tile with others: a window as wide as its type sees all that came before."""
+    check_prompt([40, 9, 5], [17, 100, 3], 2, 2, 64, 16, "bf16", "f32", window=window, sinks=sinks)
+
+
 def test_prompt_many_requests():
     rng = np.random.default_rng(5)
     new = rng.integers(0, 3, 150).tolist()
@@ -356,3 +362,10 @@ def test_shared_ignores_what_lies_outside(kind):
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_shared_long_prefix_is_split(dt, kind):
     check_shared([4010, 4200, 4100], [0, 3], [4000], 1, 4, 64, 64, kind, dt)
+
+
+@pytest.mark.parametrize("start", [[0, 4, 4, 0, 2], [4, 2, 4, 1, 4]])
+def test_shared_groups_that_do_not_ascend_are_not_looked_up_behind_the_requests(start):
+    """What such groups give is undefined, but every row is written, and from the buffers of the call alone."""
+    out, lse, _, _ = run_shared([40, 50, 60, 70], start, [16, 8, 24, 12], 2, 2, 64, 8, "bf16", "f32", common=False)
+    assert not (out == 7.0).all(-1).any() and not (lse == 7.0).any()
