@@ -141,6 +141,8 @@ bitq_status check_prompt(const bitq_prompt_desc* d) {
     if (d->requests < 1 || d->requests > 8192) return fail(BITQ_E_SHAPE, "requests=%d out of range [1, 8192]", d->requests);
     if (d->tokens < 1 || d->tokens > (1 << 20)) return fail(BITQ_E_SHAPE, "tokens=%d out of range [1, 2^20]", d->tokens);
     if (static_cast<int64_t>(d->tokens) * d->heads > (1 << 26)) return fail(BITQ_E_SHAPE, "tokens * heads is larger than 2^26");
+    if (static_cast<int64_t>(d->requests) * d->kv.kv_heads > (1 << 23))  // (a launch has fewer than 2^32 threads)
+        return fail(BITQ_E_SHAPE, "requests * kv_heads is larger than 2^23");
     if (d->table_stride < 1) return fail(BITQ_E_SHAPE, "table_stride=%d must be positive", d->table_stride);
     if (d->max_len < 1 || d->max_len > static_cast<int64_t>(d->table_stride) * d->kv.page)
         return fail(BITQ_E_SHAPE, "max_len=%d out of range [1, table_stride * page]", d->max_len);
@@ -198,7 +200,7 @@ bitq_status check_pages_buffers(const KvPagesLayout& L, void* result, size_t res
     return BITQ_OK;
 }
 
-bitq_status check_rows_call(const bitq_kvdesc& kv, int heads, int32_t q_dtype, int32_t out_dtype, const RowsCall& c,
+bitq_status check_rows_call(const bitq_kvdesc& kv, int heads, int64_t rows, int requests, int table_stride, int groups, int32_t q_dtype, int32_t out_dtype, const RowsCall& c,
                             size_t cache_bytes, const RowsPlan& plan, size_t ws_bytes) {
     if (!c.q || !c.cache || !c.table || !c.start || !c.lens || !c.out) return fail(BITQ_E_ARG, "a device pointer is NULL");
     if (c.q_stride < static_cast<int64_t>(heads) * kv.head_dim || c.q_stride > (int64_t(1) << 40))
@@ -214,7 +216,17 @@ bitq_status check_rows_call(const bitq_kvdesc& kv, int heads, int32_t q_dtype, i
         if (!aligned(c.ws, 256)) return fail(BITQ_E_ALIGN, "workspace must be 256-byte aligned");
         if (ws_bytes < plan.ws_bytes) return fail(BITQ_E_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, plan.ws_bytes);
     }
-    return BITQ_OK;
+    const size_t row = static_cast<size_t>(heads) * kv.head_dim, r = 4 * static_cast<size_t>(requests), n = static_cast<size_t>(rows);
+    const Range in[] = {{c.q, ((n - 1) * c.q_stride + row) * dtype_align(q_dtype), "q_dev"},
+                        {c.cache, need, "cache_dev"},
+                        {c.table, r * table_stride, "table_dev"},
+                        {c.lens, r, "lens_dev"},
+                        {c.start, 4 * (static_cast<size_t>(groups ? groups : requests) + 1), "start_dev"},
+                        {c.prefix, 4 * static_cast<size_t>(groups), "prefix_dev"}};
+    const Range out[] = {{c.out, n * row * dtype_align(out_dtype), "out_dev"},
+                         {c.lse, c.lse ? n * heads * 4 : 0, "lse_dev"},
+                         {plan.ws_bytes ? c.ws : nullptr, plan.ws_bytes, "workspace"}};
+    return check_apart(in, out);
 }
 
 bitq_status check_device() {
@@ -617,7 +629,9 @@ bitq_status bitq_prompt_attn(const bitq_prompt_desc* desc, const void* q_dev, in
     if (bitq_status s = check_prompt(desc)) return s;
     const RowsCall c{q_dev, q_stride, cache_dev, table_dev, start_dev, lens_dev, nullptr, out_dev, lse_dev, ws_dev};
     const RowsPlan plan = prompt_plan(*desc);
-    if (bitq_status s = check_rows_call(desc->kv, desc->heads, desc->q_dtype, desc->out_dtype, c, cache_bytes, plan, ws_bytes)) return s;
+    if (bitq_status s = check_rows_call(desc->kv, desc->heads, desc->tokens, desc->requests, desc->table_stride, 0, desc->q_dtype, desc->out_dtype, c,
+                                        cache_bytes, plan, ws_bytes))
+        return s;
     if (bitq_status s = check_device()) return s;
     return launched(launch_prompt_attn(*desc, plan, c, stream));
 }
@@ -632,7 +646,9 @@ bitq_status bitq_shared_attn(const bitq_shared_desc* desc, const void* q_dev, in
     const RowsCall c{q_dev, q_stride, cache_dev, table_dev, start_dev, lens_dev, prefix_dev, out_dev, lse_dev, ws_dev};
     const RowsPlan plan = shared_plan(*desc);
     const bitq_attn_desc& d = desc->attn;
-    if (bitq_status s = check_rows_call(d.kv, d.heads, d.q_dtype, d.out_dtype, c, cache_bytes, plan, ws_bytes)) return s;
+    if (bitq_status s = check_rows_call(d.kv, d.heads, d.requests, d.requests, d.table_stride, desc->groups, d.q_dtype, d.out_dtype, c, cache_bytes,
+                                        plan, ws_bytes))
+        return s;
     if (bitq_status s = check_device()) return s;
     return launched(launch_shared_attn(*desc, plan, c, stream));
 }

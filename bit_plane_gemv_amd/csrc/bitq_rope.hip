@@ -267,9 +267,12 @@ int launch_qk_rope(const bitq_rope_desc& d, const RopeRows (&rows)[4], const voi
     // 128, bf16, us with 1 / 2 / 4 / 8 passes 40.8 / 36.7 / 39.4 / 39.0
     const int64_t waves = static_cast<int64_t>(d.tokens) * ((d.q_heads + hpw - 1) / hpw + (d.k_heads + hpw - 1) / hpw);
     a.passes = waves >= 16384 ? 2 : 1;
-    a.q_groups = (d.q_heads + hpw * a.passes - 1) / (hpw * a.passes);
-    a.k_groups = (d.k_heads + hpw * a.passes - 1) / (hpw * a.passes);
-    const int64_t items = static_cast<int64_t>(d.tokens) * (a.q_groups + a.k_groups);  // (< 2^29)
+    auto groups = [&](int heads) { return (heads + hpw * a.passes - 1) / (hpw * a.passes); };
+    auto items_of = [&] { return static_cast<int64_t>(d.tokens) * (groups(d.q_heads) + groups(d.k_heads)); };
+    while (items_of() > (int64_t(1) << 25) && a.passes < 16) a.passes *= 2;  // (a launch has fewer than 2^32 threads)
+    a.q_groups = groups(d.q_heads);
+    a.k_groups = groups(d.k_heads);
+    const int64_t items = items_of();
     const dim3 grid(static_cast<unsigned>((items + 3) / 4));
     // parts of 8 elements, all of them whole and 16-byte aligned
     const int es = d.x_dtype == BITQ_DT_F32 ? 4 : 2, eo = d.out_dtype == BITQ_DT_F32 ? 4 : 2;

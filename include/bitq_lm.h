@@ -194,7 +194,7 @@ bitq_status bitq_paged_attn(const bitq_attn_desc* desc, const void* q_dev, int64
 typedef struct {
     bitq_kvdesc kv;
     int32_t heads;         /* query heads, a multiple of kv_heads, <= 16384 */
-    int32_t requests;      /* R, 1 .. 8192 */
+    int32_t requests;      /* R, 1 .. 8192; requests * kv_heads <= 2^23 */
     int32_t tokens;        /* T: rows of q, 1 .. 2^20; tokens * heads <= 2^26 */
     int32_t table_stride;  /* entries of one request's row of the table */
     int32_t max_len;       /* most tokens of a request, 1 .. table_stride * page */
@@ -225,7 +225,8 @@ bitq_status bitq_prompt_attn_workspace(const bitq_prompt_desc* desc, size_t* byt
  *   out_dev   [T][heads][head_dim] in out_dtype, contiguous
  *   lse_dev   f32 [T][heads] log(sum_t p_t), or NULL
  * A row that sees no token gives out = 0 and lse = -inf; rows outside
- * start[0] .. start[R]-1 are left as they were.  Whatever the cache holds in
+ * start[0] .. start[R]-1 are left as they were.  out_dev, lse_dev and ws_dev
+ * may not overlap another buffer of the call.  Whatever the cache holds in
  * places that a row does not see, infinities and NaN included, has no effect
  * on it.  NaN in its own q or in keys or values that it sees gives NaN; so may
  * an infinity there.
@@ -392,6 +393,7 @@ bitq_status bitq_rope_table(const bitq_rope_freq* freq, uint64_t* table);
 /*
  * Queries and keys of new tokens, head by head:
  *   x' = w (.) x / sqrt(mean(x^2) + eps)   (x' = x without w)
+ * (squares and their sum in fp32: elements up to 2^59)
  * and the first rot elements of x' rotated, each pair (u, v) by its angle
  * a = position * f_i:
  *   (mscale (u cos a - v sin a), mscale (v cos a + u sin a))

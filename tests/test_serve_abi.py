@@ -101,6 +101,24 @@ def test_attention_arguments(fn, desc, names, cache, ws):
     assert status(fn, None, *[P] * len(names), None) == bq.E_ARG
 
 
+@pytest.mark.parametrize("fn,desc,names,cache,ws", attention_calls(), ids=["prompt", "shared"])
+def test_attention_outputs_lie_apart(fn, desc, names, cache, ws):
+    sep = {n: P + (i << 32) for i, n in enumerate(names)} | dict(stride=512, bytes=cache, lse=P + (1 << 40), ws_bytes=ws)
+    order = [n for n in names if n != "lse"]
+    for o in ("out", "lse", "ws"):
+        for n in order:
+            if n in (o, "stride", "bytes", "ws_bytes"):
+                continue
+            a = sep | {o: sep[n]}
+            assert status(fn, desc, *(a[m] for m in names), None) == bq.E_ARG, (o, n)
+
+
+def test_prompt_tiles_fit_a_launch():
+    d = dict(heads=2048, requests=8192, tokens=1, table_stride=8, max_len=8)
+    assert size("bitq_prompt_attn_workspace", prompt(kv(kv_heads=2048, page=8, pages=1), **d))[0] == bq.E_SHAPE
+    assert size("bitq_prompt_attn_workspace", prompt(kv(kv_heads=1024, page=8, pages=1), **d))[0] == bq.OK
+
+
 def test_attention_workspaces_stay_bounded():
     """Partial results take 256 MB at most, whatever the sizes; whole prompts need none."""
     for H, G, D in ((1, 1, 64), (8, 8, 128), (32, 4, 256), (1, 128, 128)):
