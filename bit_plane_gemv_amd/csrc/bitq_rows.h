@@ -44,8 +44,8 @@ namespace bitq {
 //
 // Bound: RW = 1 by the memory (64 single tokens in a window of 2048, 64 heads on 8
 // of 128, bf16: 99 us, 5.4 TB/s).  RW = 4 by the products and the softmax beside
-// them: a prompt of 4096 tokens, 32 heads of 128 on 8, bf16, 194 us, 708 TFLOP/s
-// of the formula's products, 1060 with the second term of p (a large library
+// them: a prompt of 4096 tokens, 32 heads of 128 on 8, bf16, 192 us, 715 TFLOP/s
+// of the formula's products, 1070 with the second term of p (a large library
 // product: 1426).  Of a block of 64 tokens x 32 rows the products take 1536
 // cycles of a SIMD, its 250 vector instructions some 1200; two waves share it
 // (one wave a SIMD: 340 us).  Taken out for comparison, us of 217 at that time: the
