@@ -226,8 +226,8 @@ constexpr int rows_lds(int kv_dtype, int nc, int rw) {
     const int join = rw == 4 ? 0 : w * 32 * (32 * nc + 6) * 4;
     return stages > join ? stages : join;
 }
-constexpr int rows_groups_per_cu(int kv_dtype, int nc, bool f32, int rw) {
-    const int per_simd = (8 * (f32 ? 3 : 1) + 16) * nc <= 100 && (rw == 4 || nc <= 2) ? 2 : 1;
+constexpr int rows_groups_per_cu(int kv_dtype, int nc, bool q32, int rw) {
+    const int per_simd = (8 * (q32 ? 3 : 1) + 16) * nc <= 100 && (rw == 4 || nc <= 2) ? 2 : 1;
     const int by_lds = 160 * 1024 / (rows_lds(kv_dtype, nc, rw) + 1024), by_waves = per_simd * 4 / rows_waves(rw);
     return by_lds < by_waves ? by_lds : by_waves;
 }
@@ -263,8 +263,8 @@ struct RowsCall {
 int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream);
 int launch_shared_attn(const bitq_shared_desc& d, const RowsPlan& plan, const RowsCall& c, void* stream);
 struct RowsArgs;
-void launch_rows_bf16(const RowsArgs& a, int nc, bool f32, int rw, unsigned grid, void* stream);
-void launch_rows_int8(const RowsArgs& a, int nc, bool f32, int rw, unsigned grid, void* stream);
+void launch_rows_bf16(const RowsArgs& a, int nc, bool q32, int rw, unsigned grid, void* stream);
+void launch_rows_int8(const RowsArgs& a, int nc, bool q32, int rw, unsigned grid, void* stream);
 
 // Byte layouts of the result buffer and of the workspace of bitq_kv_fork and
 // bitq_kv_compact (bitq_pages.hip).

@@ -262,7 +262,7 @@ RowsPlan prompt_plan(const bitq_prompt_desc& d) {
     p.Dp = static_cast<int>(round_up(d.kv.head_dim, 32));
     p.group = d.heads / d.kv.kv_heads;
     const int nc = p.Dp / 32;
-    const bool f32 = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    const bool q32 = d.q_dtype == BITQ_DT_F32;
     const int64_t rows = static_cast<int64_t>(d.tokens) * p.group;  // of a key-value head
     p.main.rw = rows <= 32 * static_cast<int64_t>(d.requests) ? 1 : 4;
     p.main.tiles = static_cast<int>(rows / (32 * p.main.rw) + d.requests);
@@ -271,7 +271,7 @@ RowsPlan prompt_plan(const bitq_prompt_desc& d) {
     const int64_t cap = std::min<int64_t>(512, (int64_t(1) << 26) / (static_cast<int64_t>(d.tokens) * d.heads * (p.Dp + 2)));
     // (tiles in use: one for each request with tokens at least)
     p.main.pieces = rows_pieces(std::max<int64_t>(std::min(d.requests, d.tokens), (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), span, d.kv.kv_heads,
-                                rows_groups_per_cu(d.kv.dtype, nc, f32, p.main.rw), p.main.rw, nc, cap);
+                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, nc, cap);
     if (p.main.pieces > 1) {
         p.all = p.main.pieces;
         rows_workspace(p, static_cast<int64_t>(d.tokens) * d.heads);
@@ -285,7 +285,7 @@ RowsPlan shared_plan(const bitq_shared_desc& s) {
     p.Dp = static_cast<int>(round_up(d.kv.head_dim, 32));
     p.group = d.heads / d.kv.kv_heads;
     const int nc = p.Dp / 32, H = d.kv.kv_heads;
-    const bool f32 = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    const bool q32 = d.q_dtype == BITQ_DT_F32;
     const int64_t rows = static_cast<int64_t>(d.requests) * p.group;
     p.main.rw = rows <= 32 * static_cast<int64_t>(s.groups) ? 1 : 4;
     p.main.tiles = static_cast<int>(rows / (32 * p.main.rw) + s.groups);
@@ -297,9 +297,9 @@ RowsPlan shared_plan(const bitq_shared_desc& s) {
     // (partial results of at most 256 MB; 2^23 rows: one piece of each)
     const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(512, (int64_t(1) << 25) / (static_cast<int64_t>(d.requests) * d.heads * (p.Dp + 2))));
     p.main.pieces = rows_pieces(std::max<int64_t>(s.groups, (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), s.max_prefix, H,
-                                rows_groups_per_cu(d.kv.dtype, nc, f32, p.main.rw), p.main.rw, nc, cap);
+                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, nc, cap);
     p.own.pieces = rows_pieces(p.own.tiles, std::max(d.max_len - s.max_prefix, 1), H,
-                               rows_groups_per_cu(d.kv.dtype, nc, f32, p.own.rw), p.own.rw, nc, cap);
+                               rows_groups_per_cu(d.kv.dtype, nc, q32, p.own.rw), p.own.rw, nc, cap);
     p.all = p.main.pieces + p.own.pieces;
     rows_workspace(p, static_cast<int64_t>(d.requests) * d.heads);
     return p;

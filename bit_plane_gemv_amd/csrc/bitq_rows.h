@@ -54,12 +54,12 @@ namespace bitq {
 //
 // Precision.  Cache rows are exact in bf16; int8 scales are applied in fp32, to
 // the scores and to p.  fp32 q is split into 3 bf16 terms, which hold its 24
-// bits.  p is split into 3 terms for fp32 outputs and into 2 for bf16 ones: 2
-// terms err by 2^-17 of each weight, 2^-8 of the output's own rounding, and cost
-// a quarter of the matrix work less.  One term would err by as much as that
-// rounding and make the kernel no faster than the softmax's own instructions
-// allow.  m follows the maximum only when it has grown by more than 2^8, which
-// changes no result (p may then be up to 2^8).
+// bits, and so is p (times V's scale), whatever the type of the outputs: with 2
+// terms, which err by up to 2^-16 of each weight, an output that is a small
+// difference of large terms loses bits that its own rounding would have kept,
+// and one bf16 output in a thousand rounds to its other neighbour.
+// m follows the maximum only when it has grown by more than 2^8 (p may then be
+// up to 2^8), which changes no result while sums stay in fp32's range.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -83,18 +83,18 @@ struct RowsArgs {
     int own_tiles, own_pieces, tps;  // shared: those of the requests' own tokens, and its tiles per request
     int all;               // partial results of a row, a prefix's pieces first; 0: no split
     float c;               // |scale| log2(e) (> 0); a negative scale turns q's sign
-    bool negative, q32, qvec, ovec;  // q32: fp32 q
+    bool negative, qvec, ovec;
     int odt;
 };
 
-template <int KVT, int NC, bool F32, int RW>
+template <int KVT, int NC, bool Q32, int RW>
 struct RowsShape {
     static constexpr bool I8 = KVT == BITQ_KV_INT8;
     static constexpr int Dp = 32 * NC, ES = I8 ? 1 : 2;
     static constexpr int W = rows_waves(RW);
     static constexpr int BT = rows_block(RW);  // tokens of a block
     static constexpr int ROWS = 32 * RW;
-    static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
+    static constexpr int NQ = Q32 ? 3 : 1, NP = 3;
     static constexpr int KB = BT * Dp * ES, STAGE = 2 * KB + (I8 ? 8 * BT : 0);
     static constexpr int TEAMS = RW == 4 ? 1 : W;
     static constexpr int GROUPS = BT / 8 / (RW == 4 ? W : 1);  // groups of 8 tokens that a wave copies
@@ -261,9 +261,9 @@ __device__ __forceinline__ float rows_lse(float m, float l) {
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int KVT, int NC, bool F32, int RW>
-__global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F32, RW) * rows_waves(RW) + 3) / 4) void rows_attn_kernel(RowsArgs a) {
-    using Z = RowsShape<KVT, NC, F32, RW>;
+template <int KVT, int NC, bool Q32, int RW>
+__global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, Q32, RW) * rows_waves(RW) + 3) / 4) void rows_attn_kernel(RowsArgs a) {
+    using Z = RowsShape<KVT, NC, Q32, RW>;
     constexpr bool I8 = Z::I8, C8 = Z::C8;
     constexpr int Dp = Z::Dp, ES = Z::ES, W = Z::W, BT = Z::BT, NQ = Z::NQ, NP = Z::NP, CN = Z::CN, T16 = BT / 16;
     __shared__ __align__(16) uint8_t s_mem[Z::LDS];
@@ -481,8 +481,8 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         }
     };
     // (places without an element read the row's first ones, and use none of them)
-    const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qat * (a.q32 ? 4 : 2);
-    if (a.qvec && F32 && a.q32) {
+    const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qat * (Q32 ? 4 : 2);
+    if (Q32 && a.qvec) {
         queries([&](int d, bool some, float (&f)[8]) __attribute__((always_inline)) {
             const uint4* p = reinterpret_cast<const uint4*>(qp + (some ? 4 * d : 0));
             const uint4 u = p[0], v = p[1];
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, F
         queries([&](int d, bool some, float (&f)[8]) __attribute__((always_inline)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = load_act(qp, a.q32 ? BITQ_DT_F32 : BITQ_DT_BF16, min(d + e, a.D - 1));
+                const float v = load_act(qp, Q32 ? BITQ_DT_F32 : BITQ_DT_BF16, min(d + e, a.D - 1));
                 f[e] = some && d + e < a.D ? v : 0.0f;
             }
         });

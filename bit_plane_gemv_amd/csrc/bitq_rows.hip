@@ -113,17 +113,16 @@ static RowsArgs rows_args(const bitq_kvdesc& kv, const RowsPlan& plan, const Row
     a.c = mag < FLT_MIN ? FLT_MIN : mag > FLT_MAX ? FLT_MAX : mag;
     a.negative = s < 0;
     a.odt = out_dtype;
-    a.q32 = q_dtype == BITQ_DT_F32;
     const int per16 = q_dtype == BITQ_DT_F32 ? 4 : 8;
     a.qvec = a.D % 8 == 0 && c.q_stride % per16 == 0 && aligned(c.q, 16);
     a.ovec = a.D % 8 == 0 && aligned(c.out, 16);
     return a;
 }
 
-static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, int rw, bool f32, void* stream) {
+static void launch_main(const bitq_kvdesc& kv, const RowsArgs& a, int rw, bool q32, void* stream) {
     const unsigned grid = (static_cast<unsigned>(a.tiles) * a.pieces + static_cast<unsigned>(a.own_tiles) * a.own_pieces) * a.H;
-    if (kv.dtype == BITQ_KV_BF16) launch_rows_bf16(a, (a.D + 31) / 32, f32, rw, grid, stream);
-    else launch_rows_int8(a, (a.D + 31) / 32, f32, rw, grid, stream);
+    if (kv.dtype == BITQ_KV_BF16) launch_rows_bf16(a, (a.D + 31) / 32, q32, rw, grid, stream);
+    else launch_rows_int8(a, (a.D + 31) / 32, q32, rw, grid, stream);
 }
 
 template <int NE>
@@ -144,7 +143,7 @@ int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const Ro
     a.R = d.requests, a.T = d.tokens;
     a.table_stride = d.table_stride, a.max_len = d.max_len, a.window = d.window, a.sinks = d.window ? d.sinks : 0;
     a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
-    launch_main(d.kv, a, plan.main.rw, d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32, stream);
+    launch_main(d.kv, a, plan.main.rw, d.q_dtype == BITQ_DT_F32, stream);
     if (plan.all) launch_rows_join(a, plan.Dp, stream);
     return static_cast<int>(hipGetLastError());
 }
@@ -152,19 +151,19 @@ int launch_prompt_attn(const bitq_prompt_desc& d, const RowsPlan& plan, const Ro
 int launch_shared_attn(const bitq_shared_desc& s, const RowsPlan& plan, const RowsCall& c, void* stream) {
     const bitq_attn_desc& d = s.attn;
     RowsArgs a = rows_args(d.kv, plan, c, d.heads, d.q_dtype, d.out_dtype, d.scale);
-    const bool f32 = d.q_dtype == BITQ_DT_F32 || d.out_dtype == BITQ_DT_F32;
+    const bool q32 = d.q_dtype == BITQ_DT_F32;
     a.R = a.T = d.requests, a.groups = s.groups, a.max_prefix = s.max_prefix;
     a.table_stride = d.table_stride, a.max_len = d.max_len;
     a.tiles = plan.main.tiles, a.pieces = plan.main.pieces;
     a.own_tiles = plan.own.tiles, a.own_pieces = plan.own.pieces, a.tps = plan.own.tiles / d.requests;
     if (plan.main.rw == plan.own.rw) {
-        launch_main(d.kv, a, plan.main.rw, f32, stream);
+        launch_main(d.kv, a, plan.main.rw, q32, stream);
     } else {
         a.own_tiles = 0;
-        launch_main(d.kv, a, plan.main.rw, f32, stream);
+        launch_main(d.kv, a, plan.main.rw, q32, stream);
         a.tiles = 0;
         a.own_tiles = plan.own.tiles;
-        launch_main(d.kv, a, plan.own.rw, f32, stream);
+        launch_main(d.kv, a, plan.own.rw, q32, stream);
     }
     launch_rows_join(a, plan.Dp, stream);
     return static_cast<int>(hipGetLastError());
