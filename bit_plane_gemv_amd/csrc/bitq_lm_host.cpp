@@ -133,6 +133,9 @@ bitq_status check_rope(const bitq_rope_desc* d) {
     return BITQ_OK;
 }
 
+// (the factor of scores in powers of two)
+bool scale_fits(float scale) { return std::isfinite(scale * 1.44269504088896340736f); }
+
 bitq_status check_prompt(const bitq_prompt_desc* d) {
     if (!d) return fail(BITQ_E_ARG, "desc is NULL");
     if (bitq_status s = check_kv(d->kv)) return s;
@@ -153,7 +156,7 @@ bitq_status check_prompt(const bitq_prompt_desc* d) {
     if ((d->q_dtype != BITQ_DT_F32 && d->q_dtype != BITQ_DT_BF16) ||
         (d->out_dtype != BITQ_DT_F32 && d->out_dtype != BITQ_DT_BF16))
         return fail(BITQ_E_ARG, "q_dtype and out_dtype must be BITQ_DT_F32 or BITQ_DT_BF16");
-    if (!std::isfinite(d->scale)) return fail(BITQ_E_ARG, "scale is not finite");
+    if (!scale_fits(d->scale)) return fail(BITQ_E_ARG, "scale * log2(e) is not finite");
     return BITQ_OK;
 }
 
@@ -162,6 +165,7 @@ bitq_status check_shared(const bitq_shared_desc* d) {
     if (bitq_status s = check_attn(&d->attn)) return s;
     if (d->attn.requests > 8192) return fail(BITQ_E_SHAPE, "requests=%d out of range [1, 8192]", d->attn.requests);
     if (d->attn.window != 0) return fail(BITQ_E_SHAPE, "window=%d: a shared prefix is seen whole", d->attn.window);
+    if (!scale_fits(d->attn.scale)) return fail(BITQ_E_ARG, "scale * log2(e) is not finite");
     if (d->groups < 1 || d->groups > d->attn.requests) return fail(BITQ_E_SHAPE, "groups=%d out of range [1, requests]", d->groups);
     if (d->max_prefix < 1 || d->max_prefix > d->attn.max_len)
         return fail(BITQ_E_SHAPE, "max_prefix=%d out of range [1, max_len]", d->max_prefix);

@@ -609,6 +609,18 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, Q
 #pragma unroll
         for (int i = 0; i < 8 * T16; ++i) mx = fmaxf(mx, x[i]);
         mx = fmaxf(pair_max(mx) * a.c, -FLT_MAX);
+        // An exponent c x - m is rounded once, but m is the rounded maximum: the largest exponent is the rounding error of m, a
+        // factor that all of a row's weights have in common while it is below 1.  Where scores are larger than 2^24 it could
+        // take them out of range: such rows have x scaled and rounded before m is subtracted.
+        const bool far = fabsf(mx) > 0x1p24f && mx > -FLT_MAX;
+        float c = a.c;
+        if (__any(far)) {
+            asm volatile("");  // (a branch, not products in every block)
+            const float f = far ? a.c : 1.0f;
+            c = far ? 1.0f : a.c;
+#pragma unroll
+            for (int i = 0; i < 8 * T16; ++i) x[i] *= f;
+        }
         if (__any(mx > m + 8.0f)) {  // (each row by its own maximum: its result depends on no other row)
             const float mn = mx > m + 8.0f ? mx : m, f = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
@@ -622,7 +634,7 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, Q
         auto weights = [&](int t, bf16x8_t (&pf)[NP]) __attribute__((always_inline)) {
             float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * t + e], a.c, -m));
+            for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * t + e], c, -m));
             l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             if constexpr (I8) {
                 const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(sc + (2 * t + h) * 16 + 8);

@@ -110,7 +110,7 @@ static RowsArgs rows_args(const bitq_kvdesc& kv, const RowsPlan& plan, const Row
     a.all = plan.all;
     // (a scale of 0 weighs all tokens alike: so does one so small that no score counts)
     const float s = scale * 1.44269504088896340736f, mag = s < 0 ? -s : s;
-    a.c = mag < FLT_MIN ? FLT_MIN : mag > FLT_MAX ? FLT_MAX : mag;
+    a.c = mag < FLT_MIN ? FLT_MIN : mag;
     a.negative = s < 0;
     a.odt = out_dtype;
     const int per16 = q_dtype == BITQ_DT_F32 ? 4 : 8;

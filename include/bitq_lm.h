@@ -202,7 +202,7 @@ typedef struct {
     int32_t sinks;         /* first tokens that stay visible; 0 without a window */
     int32_t q_dtype;       /* BITQ_DT_F32 or BITQ_DT_BF16 */
     int32_t out_dtype;     /* BITQ_DT_F32 or BITQ_DT_BF16 */
-    float scale;           /* finite */
+    float scale;           /* scale log2(e) finite */
 } bitq_prompt_desc;
 
 /* Workspace of bitq_prompt_attn: partial results where tokens are split over
@@ -229,7 +229,10 @@ bitq_status bitq_prompt_attn_workspace(const bitq_prompt_desc* desc, size_t* byt
  * may not overlap another buffer of the call.  Whatever the cache holds in
  * places that a row does not see, infinities and NaN included, has no effect
  * on it.  NaN in its own q or in keys or values that it sees gives NaN; so may
- * an infinity there.
+ * an infinity there.  Scores are held as fp32 numbers, in powers of two: one for
+ * which scale log2(e) q . K is beyond fp32 counts as an infinity.  So are weights
+ * times values before the division by their sum: tokens that a row sees, times
+ * the largest of their values, up to 2^119.
  */
 bitq_status bitq_prompt_attn(const bitq_prompt_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
                              size_t cache_bytes, const int32_t* table_dev, const int32_t* start_dev,
@@ -245,7 +248,7 @@ bitq_status bitq_prompt_attn(const bitq_prompt_desc* desc, const void* q_dev, in
  * copies).  Requests in no group have no prefix.
  */
 typedef struct {
-    bitq_attn_desc attn;   /* window = 0; requests <= 8192 */
+    bitq_attn_desc attn;   /* window = 0; requests <= 8192; scale log2(e) finite */
     int32_t groups;        /* 1 .. requests */
     int32_t max_prefix;    /* most tokens of a prefix, 1 .. attn.max_len */
 } bitq_shared_desc;
@@ -259,6 +262,7 @@ bitq_status bitq_shared_attn_workspace(const bitq_shared_desc* desc, size_t* byt
  *              (where they do not ascend, as for bitq_prompt_attn)
  *   prefix_dev i32 [groups], 0 .. max_prefix (others count as the nearer end)
  * A request shorter than its group's prefix sees its own length of it.
+ * Scores and values as for bitq_prompt_attn.
  */
 bitq_status bitq_shared_attn(const bitq_shared_desc* desc, const void* q_dev, int64_t q_stride, const void* cache_dev,
                              size_t cache_bytes, const int32_t* table_dev, const int32_t* lens_dev,

@@ -114,3 +114,29 @@ def test_shared_largest_score_takes_all(scale, factor, R, G, dt, kind):
         t = int(np.argmax(x * np.sign(scale)))
         return t, x[t]
     check(out, lse, q0, top, scale, sections[1], sections[3], lambda i, t: (int(table[i, t // PAGE]), t % PAGE), DT[dt][1], G)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [2, 40])
+def test_prompt_rows_beside_one_of_large_scores_keep_their_bits(new, dt, kind):
+    rng = np.random.default_rng(new)
+    H, G, lens = 2, 4, [200]
+    table, pool = tables(lens, PAGE, 13, rng)
+    sections = lm.cache_sections(pool, H, PAGE, D, kind == "int8", rng)
+    kv = bq.kvdesc(H, D, PAGE, pool, bq.KV_INT8 if kind == "int8" else bq.KV_BF16)
+    cache = upload(sections, kv)
+    q = torch.from_numpy(rng.standard_normal((new, H * G, D)).astype(np.float32)).to(DT[dt][1])
+    d = bq.prompt_desc(kv, H * G, 1, new, 13, 200, q_dtype=DT[dt][0], out_dtype=DT[dt][0])
+    ws = torch.empty(max(1, bq.prompt_attn_workspace(d)), dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    say("prompt one row of large scores", new, dt, kind)
+    got = []
+    for factor in (1.0, 1e20):
+        x = q.clone()
+        x[new // 2, 1] *= factor
+        out, lse = torch.full((new, H * G, D), 7.0, dtype=DT[dt][1], device="cuda"), torch.full((new, H * G), 7.0, device="cuda")
+        bq.prompt_attn(d, x.cuda(), cache, torch.from_numpy(table).cuda(), i32([0, new]), i32(lens), out, ws, lse=lse)
+        out[new // 2, 1], lse[new // 2, 1] = 0, 0
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
