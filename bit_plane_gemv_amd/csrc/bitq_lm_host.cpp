@@ -484,17 +484,17 @@ bitq_status bitq_rope_table(const bitq_rope_freq* f, uint64_t* table) {
     const long double tau = 6.283185307179586476925286766559005768L;
     const int rot = f->rot;
     // where a pair makes x turns over the trained positions (a number of a pair)
-    auto at = [&](double x) { return rot * std::log(f->trained / (x * 2 * M_PI)) / (2 * std::log(f->base)); };
-    double lo = 0, hi = 1;
+    auto at = [&](long double x) { return rot * std::log(f->trained / (x * tau)) / (2 * std::log(static_cast<long double>(f->base))); };
+    long double lo = 0, hi = 1;
     if (f->kind == BITQ_ROPE_RAMP) {
-        lo = std::max(std::floor(at(f->turns_keep)), 0.0);
-        hi = std::min(std::ceil(at(f->turns_scale)), static_cast<double>(rot - 1));
+        lo = std::max(std::floor(at(f->turns_keep)), 0.0L);
+        hi = std::min(std::ceil(at(f->turns_scale)), static_cast<long double>(rot - 1));
     }
     for (int i = 0; i < rot / 2; ++i) {
         const long double w = std::pow(static_cast<long double>(f->base), -2.0L * i / rot);
         long double keep = 1;  // how much of the plain frequency stays
         if (f->kind == BITQ_ROPE_LINEAR) keep = 0;
-        if (f->kind == BITQ_ROPE_RAMP) keep = 1 - std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+        if (f->kind == BITQ_ROPE_RAMP) keep = 1 - std::min(std::max((i - lo) / std::max(hi - lo, 0.001L), 0.0L), 1.0L);
         if (f->kind == BITQ_ROPE_BAND) {
             const long double t = (f->trained * w / tau - f->turns_scale) / (f->turns_keep - f->turns_scale);
             keep = std::min(std::max(t, 0.0L), 1.0L);

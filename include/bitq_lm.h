@@ -388,9 +388,11 @@ typedef struct {
 
 /*
  * Host only.  table receives rot/2 entries: the fraction of a turn per position
- * as a 64-bit fixed-point number, round(f_i / (2 pi) 2^64) mod 2^64 (a program
- * with frequencies of its own fills the table in itself).  Angles are then
- * exact to 2^-32 turns at every position below 2^31.
+ * as a 64-bit fixed-point number, f_i / (2 pi) 2^64 mod 2^64 rounded (computed
+ * with 64 bits: off by less than 1/2 + 12 f_i / (2 pi) units; a program with
+ * frequencies of its own fills the table in itself).  bitq_qk_rope cuts position
+ * times entry to 32 bits of a turn: for frequencies up to 1, angles are off by
+ * less than 2^-30 turns at every position below 2^31.
  */
 bitq_status bitq_rope_table(const bitq_rope_freq* freq, uint64_t* table);
 
