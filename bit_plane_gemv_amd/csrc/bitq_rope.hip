@@ -18,7 +18,7 @@ namespace bitq {
 //
 // Angles.  table holds each pair's turns per position as a fraction of 2^64;
 // position * entry mod 2^64 is the angle with no error beyond the entry's own
-// (2^-63 turns per position at most), wherever the position.  Its upper 32 bits are
+// (below 2^-62 turns per position), wherever the position.  Its upper 32 bits are
 // cut into a quarter and a rest of at most an eighth of a turn, on which the
 // Taylor series of sine (to x^9) and cosine (to x^10) err by less than 2^-28.
 // An fp32 angle would be off by up to 0.004 at position 131072.
