@@ -141,11 +141,10 @@ bitq_status check_prompt(const bitq_prompt_desc* d) {
     if (bitq_status s = check_kv(d->kv)) return s;
     if (d->heads < 1 || d->heads > 16384 || d->heads % d->kv.kv_heads)
         return fail(BITQ_E_SHAPE, "heads=%d must be a multiple of kv_heads=%d, at most 16384", d->heads, d->kv.kv_heads);
+    // (8192 requests x 1024 key-value heads, with a place for a tile each: a launch has fewer than 2^32 threads)
     if (d->requests < 1 || d->requests > 8192) return fail(BITQ_E_SHAPE, "requests=%d out of range [1, 8192]", d->requests);
     if (d->tokens < 1 || d->tokens > (1 << 20)) return fail(BITQ_E_SHAPE, "tokens=%d out of range [1, 2^20]", d->tokens);
     if (static_cast<int64_t>(d->tokens) * d->heads > (1 << 26)) return fail(BITQ_E_SHAPE, "tokens * heads is larger than 2^26");
-    if (static_cast<int64_t>(d->requests) * d->kv.kv_heads > (1 << 23))  // (a launch has fewer than 2^32 threads)
-        return fail(BITQ_E_SHAPE, "requests * kv_heads is larger than 2^23");
     if (d->table_stride < 1) return fail(BITQ_E_SHAPE, "table_stride=%d must be positive", d->table_stride);
     if (d->max_len < 1 || d->max_len > static_cast<int64_t>(d->table_stride) * d->kv.page)
         return fail(BITQ_E_SHAPE, "max_len=%d out of range [1, table_stride * page]", d->max_len);

@@ -194,7 +194,7 @@ bitq_status bitq_paged_attn(const bitq_attn_desc* desc, const void* q_dev, int64
 typedef struct {
     bitq_kvdesc kv;
     int32_t heads;         /* query heads, a multiple of kv_heads, <= 16384 */
-    int32_t requests;      /* R, 1 .. 8192; requests * kv_heads <= 2^23 */
+    int32_t requests;      /* R, 1 .. 8192 */
     int32_t tokens;        /* T: rows of q, 1 .. 2^20; tokens * heads <= 2^26 */
     int32_t table_stride;  /* entries of one request's row of the table */
     int32_t max_len;       /* most tokens of a request, 1 .. table_stride * page */
