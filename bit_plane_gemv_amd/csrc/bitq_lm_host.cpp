@@ -246,10 +246,10 @@ bitq_status launched(int e) {
 }
 
 // Pieces for tiles of a call: enough workgroups to fill the GPU, each with two
-// rounds of blocks or more.
-int rows_pieces(int64_t tiles, int64_t span, int kv_heads, int groups_per_cu, int rw, int nc, int64_t most) {
+// blocks or more (128 rows: one after the other; few rows: one for each wave).
+int rows_pieces(int64_t tiles, int64_t span, int kv_heads, int groups_per_cu, int rw, int64_t most) {
     const int64_t want = 256 * groups_per_cu / std::max<int64_t>(1, tiles * kv_heads);
-    const int64_t unit = rows_block(rw) * 2;  // (128 rows: two blocks; few rows: a block for each of the two waves)
+    const int64_t unit = rows_block(rw) * 2;
     return static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(want, most), (span + unit - 1) / unit)));
 }
 
@@ -274,7 +274,7 @@ RowsPlan prompt_plan(const bitq_prompt_desc& d) {
     const int64_t cap = std::min<int64_t>(512, (int64_t(1) << 26) / (static_cast<int64_t>(d.tokens) * d.heads * (p.Dp + 2)));
     // (tiles in use: one for each request with tokens at least)
     p.main.pieces = rows_pieces(std::max<int64_t>(std::min(d.requests, d.tokens), (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), span, d.kv.kv_heads,
-                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, nc, cap);
+                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, cap);
     if (p.main.pieces > 1) {
         p.all = p.main.pieces;
         rows_workspace(p, static_cast<int64_t>(d.tokens) * d.heads);
@@ -297,12 +297,13 @@ RowsPlan shared_plan(const bitq_shared_desc& s) {
     // tiles of 128 rows).
     p.own.rw = p.group <= 32 ? 1 : 4;
     p.own.tiles = d.requests * ((p.group + 32 * p.own.rw - 1) / (32 * p.own.rw));
-    // (partial results of at most 256 MB; 2^23 rows: one piece of each)
+    // (partial results of at most 256 MB where there are few rows; a piece of the prefix and one of the own tokens always: 2^23
+    // rows of 256 elements need 17 GB)
     const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(512, (int64_t(1) << 25) / (static_cast<int64_t>(d.requests) * d.heads * (p.Dp + 2))));
     p.main.pieces = rows_pieces(std::max<int64_t>(s.groups, (rows + 32 * p.main.rw - 1) / (32 * p.main.rw)), s.max_prefix, H,
-                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, nc, cap);
+                                rows_groups_per_cu(d.kv.dtype, nc, q32, p.main.rw), p.main.rw, cap);
     p.own.pieces = rows_pieces(p.own.tiles, std::max(d.max_len - s.max_prefix, 1), H,
-                               rows_groups_per_cu(d.kv.dtype, nc, q32, p.own.rw), p.own.rw, nc, cap);
+                               rows_groups_per_cu(d.kv.dtype, nc, q32, p.own.rw), p.own.rw, cap);
     p.all = p.main.pieces + p.own.pieces;
     rows_workspace(p, static_cast<int64_t>(d.requests) * d.heads);
     return p;

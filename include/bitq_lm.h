@@ -253,7 +253,9 @@ typedef struct {
     int32_t max_prefix;    /* most tokens of a prefix, 1 .. attn.max_len */
 } bitq_shared_desc;
 
-bitq_status bitq_shared_attn_workspace(const bitq_shared_desc* desc, size_t* bytes);  /* as bitq_prompt_attn's */
+/* As bitq_prompt_attn's, but never 0: each row has a partial result of the prefix
+ * and one of its own tokens at least, requests * heads * 2 * (4 Dp + 8) bytes. */
+bitq_status bitq_shared_attn_workspace(const bitq_shared_desc* desc, size_t* bytes);
 
 /*
  * Buffers as for bitq_paged_attn, and
