@@ -288,10 +288,17 @@ inline KvPagesLayout kv_pages_layout(const bitq_kv_pages_desc& d) {
     L.ws_total = L.off_reqs + align256(16 * static_cast<size_t>(d.requests));
     return L;
 }
-// Whether one workgroup does it all (one launch instead of four or five).
+// Whether one workgroup does it all (one launch instead of four or five).  Its
+// waves take parts of 64 entries of the tables' rows, so short rows count as
+// whole parts.  us in a graph, one launch / one for each phase, of a fork and of
+// a compaction: 32 parts 8.7 / 11.3 and 8.4 / 14.0, 64 parts 10.6 / 11.5 and
+// 10.1 / 14.1, 96 parts 13.0 / 11.5 and 12.4 / 14.6, 128 parts 15.0 / 11.7 and
+// 15.7 / 14.6, 2048 parts 141 / 16 and 116 / 15 (called one by one the phases
+// take 14.4 and 16.6 or more); lists of 16384 places 11.8 / 11.6 and 10.9 / 14.4,
+// of 65536 16.0 / 11.6 and 15.1 / 15.8.
 inline bool kv_pages_small(const bitq_kv_pages_desc& d) {
     return 4 * static_cast<int64_t>(d.pool) + 16 * static_cast<int64_t>(d.requests) <= kPagesSmallLds &&
-           static_cast<int64_t>(d.requests) * d.table_stride <= 8192 && d.moves <= 65536;
+           static_cast<int64_t>(d.requests) * ((d.table_stride + int64_t(63)) / 64) <= 96 && d.moves <= 16384;
 }
 
 int launch_kv_fork(const bitq_kv_pages_desc& d, const int32_t* src, const int32_t* keep, const int32_t* len, int32_t* ring,

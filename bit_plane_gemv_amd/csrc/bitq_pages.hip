@@ -24,8 +24,9 @@ namespace bitq {
 // larger ones take a launch for each phase, with the words in the workspace.
 //
 // Bound by latency: a fork of 64 requests of up to 64 pages 10.4 us in one
-// launch (14.4 in four), of 256 requests of up to 128 pages 14.6 us in four
-// (68 in one); a compaction of 257 pages 5.5 us in one, of 16385 pages 26 us in five.
+// launch, of 256 requests of up to 128 pages 14.6 us in four; a compaction of 257
+// pages 5.5 us in one, of 16385 pages 26 us in five (both sides of the rule:
+// kv_pages_small).
 constexpr uint32_t kNone = 0xFFFFFFFFu, kHeld = 0xFFFFFFFEu;
 
 struct PagesArgs {
