@@ -262,11 +262,12 @@ int launch_qk_rope(const bitq_rope_desc& d, const RopeRows (&rows)[4], const voi
     a.lph_shift = 0;
     while ((1 << a.lph_shift) < a.units) ++a.lph_shift;
     const int hpw = 64 >> a.lph_shift;
-    // one pass for few tokens; with more waves than the GPU holds at once
-    // (8 a SIMD) two heads a lane share its angles: 4096 tokens x 72 heads of
-    // 128, bf16, us with 1 / 2 / 4 / 8 passes 40.8 / 36.7 / 39.4 / 39.0
+    // One pass while the GPU (1024 SIMDs, 5 of these waves each) holds nearly all waves at once; then two heads a lane share its
+    // angles.  us in a graph with 1 / 2 passes: 2304 waves (256 tokens x 72 heads of 128, bf16) 5.5 / 6.1, 2560 (512 x 40 of 128,
+    // fp32) 6.6 / 7.0, 4096 (1024 x 64 of 64, bf16) 6.8 / 6.5, 4608 (512 x 72) 7.8 / 7.6, 9216 13.0 / 11.7, 36864 38.8 / 31.9;
+    // 4 and 8 passes of 36864 took 7 % longer than 2.
     const int64_t waves = static_cast<int64_t>(d.tokens) * ((d.q_heads + hpw - 1) / hpw + (d.k_heads + hpw - 1) / hpw);
-    a.passes = waves >= 16384 ? 2 : 1;
+    a.passes = waves >= 4096 ? 2 : 1;
     auto groups = [&](int heads) { return (heads + hpw * a.passes - 1) / (hpw * a.passes); };
     auto items_of = [&] { return static_cast<int64_t>(d.tokens) * (groups(d.q_heads) + groups(d.k_heads)); };
     while (items_of() > (int64_t(1) << 25) && a.passes < 16) a.passes *= 2;  // (a launch has fewer than 2^32 threads)
