@@ -140,3 +140,24 @@ def test_prompt_rows_beside_one_of_large_scores_keep_their_bits(new, dt, kind):
         out[new // 2, 1], lse[new // 2, 1] = 0, 0
         got.append((out, lse))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_prompt_largest_values(new, dt):
+    """64 tokens and values of 2^113: their product is the 2^119 that sums before the division may take."""
+    rng = np.random.default_rng(new)
+    H, G, lens = 2, 4, [64]
+    table, pool = tables(lens, PAGE, 4, rng)
+    K, V, ks, vs = lm.cache_sections(pool, H, PAGE, D, False, rng)
+    V = (torch.sign(V.float()) * 2.0 ** 113).bfloat16()
+    kv = bq.kvdesc(H, D, PAGE, pool)
+    q = torch.from_numpy(rng.standard_normal((new, H * G, D)).astype(np.float32) * 4).to(DT[dt][1])
+    d = bq.prompt_desc(kv, H * G, 1, new, 4, 64, q_dtype=DT[dt][0], out_dtype=DT[dt][0])
+    ws = torch.empty(max(1, bq.prompt_attn_workspace(d)), dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full((new, H * G, D), 7.0, dtype=DT[dt][1], device="cuda")
+    say("prompt largest values", new, dt)
+    bq.prompt_attn(d, q.cuda(), upload((K, V, ks, vs), kv), torch.from_numpy(table).cuda(), i32([0, new]), i32(lens), out, ws)
+    want, _, tol, _ = ref.prompt(q.double().numpy(), (K, V, ks, vs), table, [0, new], lens, PAGE, np.float32(D ** -0.5), 0, 0, 64, 3)
+    close(out, want, tol + ref.half_step(DT[dt][1]) * (np.abs(want) + tol), "out")
