@@ -293,8 +293,8 @@ RowsPlan shared_plan(const bitq_shared_desc& s) {
     p.main.rw = rows <= 32 * static_cast<int64_t>(s.groups) ? 1 : 4;
     p.main.tiles = static_cast<int>(rows / (32 * p.main.rw) + s.groups);
     // One launch for both parts if both take few rows, so that each fills what the other leaves (40 requests in 5 groups, 32
-    // heads of 64, int8: 54 -> 48 us); else a launch each (64 requests on 16384 tokens: 95 us, and 101 with own tokens on
-    // tiles of 128 rows).
+    // heads of 64, int8: 54 -> 48 us); else a launch each (64 requests on 16384 tokens, with two
+    // terms of p: 95 us, and 101 with own tokens on tiles of 128 rows).
     p.own.rw = p.group <= 32 ? 1 : 4;
     p.own.tiles = d.requests * ((p.group + 32 * p.own.rw - 1) / (32 * p.own.rw));
     // (partial results of at most 256 MB where there are few rows; a piece of the prefix and one of the own tokens always: 2^23

@@ -28,9 +28,9 @@ namespace bitq {
 // A operand one 16-byte read.
 //
 // Tokens come in blocks that are copied straight from the cache into LDS, two
-// stages of them, one in flight while the other is worked on.  (Copies issued in
-// a row between barrier and products instead of between the products: 204
-// against 216 us.)  Copies move
+// stages of them, one in flight while the other is worked on.  Copies are issued
+// between the products (in a row before them: the same 250 us for a prompt of 4096
+// tokens, 113 against 111 us for 64 requests on a prefix of 16384).  They move
 // groups of 8 tokens (a page has whole groups), so a page's index is the same
 // for a whole copy instruction.  Keys are stored with their 16-byte pieces
 // exchanged within a row by the row's number, so that the reads of a score tile
@@ -43,14 +43,15 @@ namespace bitq {
 // A tile's tokens may be split over `pieces` workgroups; rows_join_kernel joins.
 //
 // Bound: RW = 1 by the memory (64 single tokens in a window of 2048, 64 heads on 8
-// of 128, bf16: 99 us, 5.4 TB/s).  RW = 4 by the products and the softmax beside
-// them: a prompt of 4096 tokens, 32 heads of 128 on 8, bf16, 192 us, 715 TFLOP/s
-// of the formula's products, 1070 with the second term of p (a large library
-// product: 1426).  Of a block of 64 tokens x 32 rows the products take 1536
-// cycles of a SIMD, its 250 vector instructions some 1200; two waves share it
-// (one wave a SIMD: 340 us).  Taken out for comparison, us of 217 at that time: the
-// copies 23, exponentials 13, a third of the products (one term) 50, three
-// quarters of the softmax 24, LDS reads 6.
+// of 128, bf16: 100 us, 5.4 TB/s).  RW = 4 by the products and the softmax beside
+// them: a prompt of 4096 tokens, 32 heads of 128 on 8, bf16, 239 to 250 us by the
+// card's clock, 576 TFLOP/s of the formula's products, 1150 with the three terms
+// of p (a large library product: 1426).  Of a block of 64 tokens x 32 rows the
+// products take 2048 cycles of a SIMD, its 357 vector instructions some 1430; two
+// waves share it, and a product is under way in 54 % of the cycles.  With two
+// terms of p, and taken out for comparison, us of 217 at that time: the copies 23,
+// exponentials 13, three quarters of the softmax 24, LDS reads 6; one wave a SIMD:
+// 340 us.
 //
 // Precision.  Cache rows are exact in bf16; int8 scales are applied in fp32, to
 // the scores and to p.  fp32 q is split into 3 bf16 terms, which hold its 24
@@ -603,7 +604,8 @@ __global__ __launch_bounds__(64 * rows_waves(RW), (rows_groups_per_cu(KVT, NC, Q
                 x[i] = __uint_as_float((__float_as_uint(x[i]) & yes) | (0xFF800000u & ~yes));  // else -inf
             }
         }
-        // ---- the running maximum.  (The wave that has products to issue goes first: 208 -> 199 us for a prompt of 4096.)
+        // ---- the running maximum.  (The wave that has products to issue goes first: 208 -> 199 us for a prompt of 4096, with two
+        // terms of p.)
         __builtin_amdgcn_s_setprio(0);
         float mx = -FLT_MAX;
 #pragma unroll

@@ -401,7 +401,8 @@ bitq_status bitq_rope_table(const bitq_rope_freq* freq, uint64_t* table);
 /*
  * Queries and keys of new tokens, head by head:
  *   x' = w (.) x / sqrt(mean(x^2) + eps)   (x' = x without w)
- * (squares and their sum in fp32: elements up to 2^59)
+ * (squares and their sum in fp32: elements up to 2^59, and with eps = 0 a
+ * largest one of 2^-40 or more)
  * and the first rot elements of x' rotated, each pair (u, v) by its angle
  * a = position * f_i:
  *   (mscale (u cos a - v sin a), mscale (v cos a + u sin a))
