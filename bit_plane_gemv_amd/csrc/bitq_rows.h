@@ -56,7 +56,7 @@ namespace bitq {
 // Precision.  Cache rows are exact in bf16; int8 scales are applied in fp32, to
 // the scores and to p.  fp32 q is split into 3 bf16 terms, which hold its 24
 // bits, and so is p (times V's scale), whatever the type of the outputs: with 2
-// terms, which err by up to 2^-16 of each weight, an output that is a small
+// terms, which err by up to 2^-17 of each weight, an output that is a small
 // difference of large terms loses bits that its own rounding would have kept,
 // and one bf16 output in a thousand rounds to its other neighbour.
 // m follows the maximum only when it has grown by more than 2^8 (p may then be

@@ -55,7 +55,7 @@ def queries(rows, A, factor, dt, rng):
 
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("new,length,G", [(1, 90, 4), (1, 1500, 4), (5, 170, 4), (70, 170, 4)])
+@pytest.mark.parametrize("new,length,G", [(1, 1, 4), (2, 2, 4), (1, 90, 4), (1, 1500, 4), (5, 170, 4), (70, 170, 4)])
 @pytest.mark.parametrize("scale,factor", LARGE)
 def test_prompt_largest_score_takes_all(scale, factor, new, length, G, dt, kind):
     rng = np.random.default_rng(length)
